@@ -38,6 +38,8 @@
  * State (m3_state): h (b, H, N, P) fp32, carry_B (b, H, R, N) fp32 (previous
  * token's raw B, before bias), carry_x (b, H, P) fp32 (previous token's raw x).
  * An all-zero state is a fresh sequence (no previous-token term at t = 0).
+ * Linear attention (m3_linattn_*) and the pages of a pool of states (m3_pages_*) state their
+ * layouts at their declarations.
  */
 #ifndef M3_H
 #define M3_H
@@ -289,10 +291,107 @@ m3_status m3_frontend(const m3_dims* dims, const void* B_raw, const void* C_raw,
 m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, const float* weight,
                          float eps, void* out, void* stream);
 
+/* ---- linear attention with a decay per head ---------------------------------------- */
+
+/* A recurrent layer beside the scan, as hybrid stacks use it: no rotation, no trapezoid, a decay
+ * that is a constant of the head.  Per (sequence, head h; group g = h / (H/G)), a = e^{log_decay[h]},
+ *   S_t = a S_{t-1} + k_t v_t^T,      y_t = scale S_t^T q_t,
+ * S_{-1} the given state or zero.  The dims are those of the scan with q and k in the place of C
+ * and B and v in the place of x: dims->R must be 1, dims->flags 0, dims->chunk is ignored.
+ *   q, k (b, L, G, N)   v, y (b, L, H, P)   in dims->dtype
+ *   log_decay (H) fp32, at most 0 (-inf: no memory)      state (H, N, P) fp32 per state row
+ *   lens (b) int32 or NULL: the tokens of each sequence of a padded batch (clamped to 0..L); the
+ *     tokens at and past it are not read, their outputs are zero, and the state is the one after
+ *     lens[i] tokens
+ *   pages (b) int32 or NULL: batch row i keeps its state in row pages[i] of a pool of npages state
+ *     rows (NULL: row i of b rows; npages is then ignored).  A negative page makes the row padding:
+ *     its outputs are zero and no state is touched.  So does a page past the pool, and a page that
+ *     an earlier row of the batch holds already; both also leave M3_ERR_STATE for m3_check.
+ * lens and pages need 4-byte alignment only.  Outputs must not overlap inputs.
+ * Precision: fp32 throughout; y is rounded once to dims->dtype.
+ */
+
+/* Scratch bytes m3_linattn_fwd needs for these dims (0 when it needs none). */
+m3_status m3_linattn_workspace_size(const m3_dims* dims, size_t* out_bytes);
+
+/* L tokens of every sequence.  state_in: the states before token 0, NULL for fresh sequences.
+ * state_out: the states after the last token, NULL if not wanted; it may be state_in.  L = 0
+ * copies the states.  Asynchronous on `stream`; allocates nothing. */
+m3_status m3_linattn_fwd(const m3_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                         float scale, const int32_t* lens, const float* state_in, float* state_out, int64_t npages,
+                         const int32_t* pages, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (dims->L is ignored): q_t, k_t (b, G, N), v_t, y_t (b, H, P).  Reads
+ * and rewrites the states in place, in fp32 throughout.  Asynchronous on `stream`. */
+m3_status m3_linattn_step(const m3_dims* dims, const void* q_t, const void* k_t, const void* v_t,
+                          const float* log_decay, float scale, float* state, int64_t npages, const int32_t* pages,
+                          void* y_t, void* stream);
+
+/* Scratch bytes m3_linattn_bwd needs: the segments' states and, with G < H, the heads' shares of dq
+ * and dk before they are summed. */
+m3_status m3_linattn_bwd_workspace_size(const m3_dims* dims, size_t* out_bytes);
+
+/* Gradients of sum(dy * y) + sum(dstate_out * state_out) with E_t = dL/dS_t:
+ *   E_t = a E_{t+1} + scale q_t dy_t^T  (the last token's: dstate_out + scale q dy^T),
+ *   dq_t = scale S_t dy_t,  dk_t = E_t v_t,  dv_t = E_t^T k_t,  dstate_in = a E_0.
+ * q, k, v, log_decay, scale, lens, state_in as the forward call took them (no pages).  dy, dv
+ * (b, L, H, P) and dq, dk (b, L, G, N, summed over a group's heads, in a fixed order) in
+ * dims->dtype; dstate_out (b, H, N, P) or NULL (zero); dstate_in (b, H, N, P) or NULL (not wanted),
+ * fp32.  log_decay is a constant of the model: it has no gradient here (a decay that is learned per
+ * token is the scan's A).  Gradients at and past a sequence's length are zero. */
+m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                         float scale, const int32_t* lens, const float* state_in, const void* dy,
+                         const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ---- pages of a pool of states ---------------------------------------------------- */
+
+/* A serving process keeps the recurrent states of many sequences in one pool: npages rows in every
+ * buffer of the model (each layer's h, carry_B and carry_x of an m3_state of b = npages rows, or its
+ * linear attention states).  Page i is row i of all of them.  m3_decode_step works on rows
+ * 0..b-1, so finished sequences are freed and the pool compacted; sampling several continuations
+ * of a prompt forks its page.  A live word per page (int32, device; 0 free, else live) belongs to the
+ * caller's pool.  Page lists are int32 device arrays (4-byte alignment), so whole ticks can be
+ * captured in a CUDA graph; entries the calls cannot use are skipped and leave M3_ERR_STATE for
+ * m3_check.  All calls are asynchronous on `stream`, allocate nothing and may not overlap on the GPU
+ * with other calls on the same pool. */
+#define M3_PAGES_MAX_BUF 64
+
+typedef struct {
+  int32_t npages;                   /* rows of every buffer */
+  int32_t nbuf;                     /* buffers, 1 .. M3_PAGES_MAX_BUF */
+  void* base[M3_PAGES_MAX_BUF];     /* device memory, 16-byte aligned, no two overlapping */
+  int64_t bytes[M3_PAGES_MAX_BUF];  /* bytes of a row: a positive multiple of 16 */
+} m3_pages;
+
+/* Page dst[i] becomes a copy of page src[i], in list order as if one after the other (a page may
+ * appear any number of times).  An entry with a negative page is skipped; one past the pool is
+ * skipped and recorded. */
+m3_status m3_pages_copy(const m3_pages* pool, int64_t n, const int32_t* src, const int32_t* dst, void* stream);
+
+/* dst[i] = the i-th lowest free page, which becomes live and a copy of page src[i]; with a negative
+ * src[i] it becomes all zero (a fresh sequence).  dst[i] = -1, recorded, when src[i] is not a live
+ * page of the pool (as it was before the call) or the free pages have run out; the i-th free page
+ * then stays free.  dst must not overlap src. */
+m3_status m3_pages_fork(const m3_pages* pool, int32_t* live, int64_t n, const int32_t* src, int32_t* dst,
+                        void* stream);
+
+/* The pages idx[0..n-1] become free; their contents stay until the page is taken again.  Negative
+ * entries are skipped, a page may appear twice, one past the pool is recorded. */
+m3_status m3_pages_free(const m3_pages* pool, int32_t* live, int64_t n, const int32_t* idx, void* stream);
+
+/* The live pages move to the front, in order.  map (npages): where each page went, -1 for a free one;
+ * order (npages): the page each live place came from, -1 behind them; count (2): the live pages, and
+ * the pages at the front that did not move.  live is rewritten to match.  The contents of pages behind
+ * the live ones are left as they were. */
+m3_status m3_pages_compact(const m3_pages* pool, int32_t* live, int32_t* map, int32_t* order, int32_t* count,
+                           void* stream);
+
 /* ---- status -------------------------------------------------------------- */
 
 /* Synchronise `stream`, then return (and clear) the device status word:
- * M3_OK, M3_ERR_TIMEOUT, or M3_ERR_CUDA if the stream reports an error. */
+ * M3_OK, M3_ERR_TIMEOUT, M3_ERR_STATE (a page index that m3_linattn_* or m3_pages_* could not use),
+ * or M3_ERR_CUDA if the stream reports an error. */
 m3_status m3_check(void* stream);
 
 /* Diagnostic of the error path (no counterpart in the pages): launches one CTA that waits on

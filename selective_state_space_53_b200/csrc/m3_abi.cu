@@ -5,7 +5,7 @@
 #include <cstring>
 #include <new>
 
-#include "m3_common.cuh"
+#include "m3_linattn.cuh"
 
 namespace m3 {
 __device__ int g_status = 0;
@@ -50,7 +50,8 @@ m3_status cuda_status(cudaError_t e) {
   return M3_ERR_CUDA;
 }
 
-m3_status check_dims(const m3_dims* d) {
+// The ranges of m3_dims; check_dims also asks whether the scan kernels hold these sizes.
+m3_status check_ranges(const m3_dims* d) {
   if (!d) return M3_ERR_NULL;
   if (d->b < 0 || d->L < 0 || d->H < 1 || d->G < 1 || d->R < 1 || d->R > 8) return M3_ERR_DIMS;
   if (d->P < 8 || d->P > 256 || (d->P % 8) != 0) return M3_ERR_DIMS;
@@ -60,6 +61,12 @@ m3_status check_dims(const m3_dims* d) {
   if (d->flags & ~(uint32_t)(M3_FLAG_SEQUENTIAL | M3_FLAG_ANGLE_DIRECT | M3_FLAG_RAW_INPUTS)) return M3_ERR_DIMS;
   if (d->dtype != M3_F32 && d->dtype != M3_BF16) return M3_ERR_DTYPE;
   if (d->b * (int64_t)d->H > (int64_t)0x7fffffff) return M3_ERR_DIMS;
+  return M3_OK;
+}
+
+m3_status check_dims(const m3_dims* d) {
+  const m3_status st = check_ranges(d);
+  if (st != M3_OK) return st;
   if (!m3::seq_scan_supported(d->P, d->N, d->R)) return M3_ERR_UNSUPPORTED;
   return M3_OK;
 }
@@ -159,6 +166,76 @@ WsLayout ws_layout(const m3_dims* dims) {
     w.fe_bytes = 2 * ((nbc * e + 255) & ~(size_t)255) + 3 * ((nsc * 4 + 255) & ~(size_t)255);
   }
   return w;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Dims of the linear attention: R = 1, no flags, and element offsets of every tensor within 63 bits.
+m3_status check_la_dims(const m3_dims* d) {
+  m3_status st = check_ranges(d);
+  if (st != M3_OK) return st;
+  if (d->R != 1 || d->flags != 0) return M3_ERR_DIMS;
+  if (d->L > (int64_t)0x7fffff00) return M3_ERR_DIMS;  // a token index is a 32-bit tile coordinate
+  return M3_OK;
+}
+
+// The forward pass's core without its pointers; the gradients' cores likewise.
+m3::LaCore la_forward(const m3_dims* d) {
+  m3::LaCore a{};
+  a.b = d->b;
+  a.L = d->L;
+  a.H = d->H;
+  a.KD = d->N;
+  a.VD = d->P;
+  a.hq = a.hk = d->G;
+  a.hv = d->H;
+  a.bf16 = d->dtype == M3_BF16;
+  a.out_f32 = !a.bf16;
+  a.s_upd = a.s_out = 1.0f;
+  a.s_i = d->P;
+  a.s_j = 1;
+  return a;
+}
+
+struct LaBwd {
+  m3::LaCore dq, dk, dv;
+  size_t core, part;  // scratch: the largest of the passes', and the heads' shares of dq or dk (G < H)
+};
+
+LaBwd la_backward(const m3_dims* d) {
+  LaBwd w;
+  w.dv = la_forward(d);
+  w.dv.rev = 1;
+  w.dq = w.dv;
+  w.dq.rev = 0;
+  w.dq.KD = d->P;
+  w.dq.VD = d->N;
+  w.dq.hq = w.dq.hk = d->H;
+  w.dq.hv = d->G;
+  w.dq.s_i = 1;
+  w.dq.s_j = d->P;
+  if (d->G < d->H) w.dq.out_f32 = 1;
+  w.dk = w.dq;
+  w.dk.rev = 1;
+  w.core = 0;
+  for (const m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
+    const size_t n = m3::la_core_ws_bytes(*a);
+    if (n > w.core) w.core = n;
+  }
+  w.core = (w.core + 255) & ~(size_t)255;
+  w.part = d->G < d->H ? sizeof(float) * (size_t)(d->b * d->L) * d->H * d->N : 0;
+  return w;
+}
+
+m3_status check_pool(const m3_pages* p, int64_t n) {
+  if (!p) return M3_ERR_NULL;
+  if (p->npages < 0 || p->nbuf < 1 || p->nbuf > M3_PAGES_MAX_BUF || n < 0) return M3_ERR_DIMS;
+  for (int j = 0; j < p->nbuf; ++j) {
+    if (p->bytes[j] < 16 || p->bytes[j] % 16 != 0) return M3_ERR_DIMS;
+    if (p->npages > 0 && !p->base[j]) return M3_ERR_NULL;
+    if (!aligned16(p->base[j])) return M3_ERR_ALIGN;
+  }
+  return M3_OK;
 }
 
 }  // namespace
@@ -502,6 +579,189 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
                              nullptr, nullptr, nullptr, nullptr, nullptr, const_cast<void*>(y));
   const cudaError_t e = m3::launch_output_norm(p, z, weight, eps, out, (cudaStream_t)stream);
   return cuda_status(e);
+}
+
+m3_status m3_linattn_workspace_size(const m3_dims* dims, size_t* out_bytes) {
+  m3_status st = check_la_dims(dims);
+  if (st != M3_OK) return st;
+  if (!out_bytes) return M3_ERR_NULL;
+  *out_bytes = m3::la_core_ws_bytes(la_forward(dims));
+  return M3_OK;
+}
+
+m3_status m3_linattn_fwd(const m3_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                         float scale, const int32_t* lens, const float* state_in, float* state_out, int64_t npages,
+                         const int32_t* pages, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  m3_status st = check_la_dims(dims);
+  if (st != M3_OK) return st;
+  if (dims->b == 0) return M3_OK;
+  if (pages && (npages < 0 || npages > 0x7fffffff)) return M3_ERR_DIMS;
+  if (!log_decay || (dims->L > 0 && (!q || !k || !v || !y))) return M3_ERR_NULL;
+  const void* all[] = {q, k, v, state_in, state_out, y};
+  for (const void* t : all)
+    if (t && !aligned16(t)) return M3_ERR_ALIGN;
+  if (!aligned4(log_decay) || !aligned4(lens) || !aligned4(pages)) return M3_ERR_ALIGN;
+  m3::LaCore a = la_forward(dims);
+  const size_t need = m3::la_core_ws_bytes(a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return M3_ERR_ALIGN;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = y;
+  a.s_out = scale;
+  a.log_decay = log_decay;
+  a.lens = lens;
+  a.pages = pages;
+  a.npages = npages;
+  a.s_in = state_in;
+  a.s_fin = state_out;
+  a.status = status_word();
+  if (!a.status) return M3_ERR_CUDA;
+  return cuda_status(m3::launch_la_core(a, workspace, need, (cudaStream_t)stream));
+}
+
+m3_status m3_linattn_step(const m3_dims* dims, const void* q_t, const void* k_t, const void* v_t,
+                          const float* log_decay, float scale, float* state, int64_t npages, const int32_t* pages,
+                          void* y_t, void* stream) {
+  m3_status st = check_la_dims(dims);
+  if (st != M3_OK) return st;
+  if (dims->b == 0) return M3_OK;
+  if (pages && (npages < 0 || npages > 0x7fffffff)) return M3_ERR_DIMS;
+  if (!q_t || !k_t || !v_t || !log_decay || !state || !y_t) return M3_ERR_NULL;
+  const void* all[] = {q_t, k_t, v_t, state, y_t};
+  for (const void* t : all)
+    if (!aligned16(t)) return M3_ERR_ALIGN;
+  if (!aligned4(log_decay) || !aligned4(pages)) return M3_ERR_ALIGN;
+  m3::LaStep a;
+  a.b = dims->b;
+  a.H = dims->H;
+  a.G = dims->G;
+  a.N = dims->N;
+  a.P = dims->P;
+  a.bf16 = dims->dtype == M3_BF16;
+  a.q = q_t;
+  a.k = k_t;
+  a.v = v_t;
+  a.log_decay = log_decay;
+  a.scale = scale;
+  a.state = state;
+  a.npages = npages;
+  a.pages = pages;
+  a.y = y_t;
+  a.status = status_word();
+  if (!a.status) return M3_ERR_CUDA;
+  return cuda_status(m3::launch_la_step(a, (cudaStream_t)stream));
+}
+
+m3_status m3_linattn_bwd_workspace_size(const m3_dims* dims, size_t* out_bytes) {
+  m3_status st = check_la_dims(dims);
+  if (st != M3_OK) return st;
+  if (!out_bytes) return M3_ERR_NULL;
+  const LaBwd w = la_backward(dims);
+  *out_bytes = w.core + w.part;
+  return M3_OK;
+}
+
+m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                         float scale, const int32_t* lens, const float* state_in, const void* dy,
+                         const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  m3_status st = check_la_dims(dims);
+  if (st != M3_OK) return st;
+  if (dims->b == 0) return M3_OK;
+  if (!log_decay || (dims->L > 0 && (!q || !k || !v || !dy || !dq || !dk || !dv))) return M3_ERR_NULL;
+  const void* all[] = {q, k, v, state_in, dy, dstate_out, dq, dk, dv, dstate_in};
+  for (const void* t : all)
+    if (t && !aligned16(t)) return M3_ERR_ALIGN;
+  if (!aligned4(log_decay) || !aligned4(lens)) return M3_ERR_ALIGN;
+  LaBwd w = la_backward(dims);
+  const size_t need = w.core + w.part;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return M3_ERR_ALIGN;
+  int* status = status_word();
+  if (!status) return M3_ERR_CUDA;
+  void* part = static_cast<char*>(workspace) + w.core;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int64_t NP_rows = dims->b * dims->L;
+  for (m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
+    a->log_decay = log_decay;
+    a->lens = lens;
+    a->status = status;
+  }
+  // dq = scale S dy: (dy, v, k) in time order, on the transposed states
+  w.dq.q = dy;
+  w.dq.k = v;
+  w.dq.v = k;
+  w.dq.s_out = scale;
+  w.dq.s_in = state_in;
+  w.dq.out = w.part ? part : dq;
+  // dk = E v: (v, dy, q) against time, on the transposed states
+  w.dk.q = v;
+  w.dk.k = dy;
+  w.dk.v = q;
+  w.dk.s_upd = scale;
+  w.dk.s_in = dstate_out;
+  w.dk.out = w.part ? part : dk;
+  // dv = E^T k: (k, q, dy) against time
+  w.dv.q = k;
+  w.dv.k = q;
+  w.dv.v = dy;
+  w.dv.s_upd = scale;
+  w.dv.s_in = dstate_out;
+  w.dv.s_fin = dstate_in;
+  w.dv.out = dv;
+  cudaError_t e = cudaSuccess;
+  if (dims->L > 0) {
+    e = m3::launch_la_core(w.dq, workspace, w.core, s);
+    if (e == cudaSuccess && w.part)
+      e = m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, w.dq.bf16, static_cast<float*>(part), dq, s);
+    if (e == cudaSuccess) e = m3::launch_la_core(w.dk, workspace, w.core, s);
+    if (e == cudaSuccess && w.part)
+      e = m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, w.dk.bf16, static_cast<float*>(part), dk, s);
+  }
+  if (e == cudaSuccess) e = m3::launch_la_core(w.dv, workspace, w.core, s);
+  return cuda_status(e);
+}
+
+m3_status m3_pages_copy(const m3_pages* pool, int64_t n, const int32_t* src, const int32_t* dst, void* stream) {
+  m3_status st = check_pool(pool, n);
+  if (st != M3_OK || n == 0 || pool->npages == 0) return st;
+  if (!src || !dst) return M3_ERR_NULL;
+  if (!aligned4(src) || !aligned4(dst)) return M3_ERR_ALIGN;
+  int* status = status_word();
+  if (!status) return M3_ERR_CUDA;
+  return cuda_status(m3::launch_pages_copy(*pool, n, src, dst, status, (cudaStream_t)stream));
+}
+
+m3_status m3_pages_fork(const m3_pages* pool, int32_t* live, int64_t n, const int32_t* src, int32_t* dst,
+                        void* stream) {
+  m3_status st = check_pool(pool, n);
+  if (st != M3_OK || n == 0) return st;
+  if ((!live && pool->npages > 0) || !src || !dst) return M3_ERR_NULL;
+  if (!aligned4(live) || !aligned4(src) || !aligned4(dst)) return M3_ERR_ALIGN;
+  int* status = status_word();
+  if (!status) return M3_ERR_CUDA;
+  return cuda_status(m3::launch_pages_fork(*pool, live, n, src, dst, status, (cudaStream_t)stream));
+}
+
+m3_status m3_pages_free(const m3_pages* pool, int32_t* live, int64_t n, const int32_t* idx, void* stream) {
+  m3_status st = check_pool(pool, n);
+  if (st != M3_OK || n == 0 || pool->npages == 0) return st;
+  if (!live || !idx) return M3_ERR_NULL;
+  if (!aligned4(live) || !aligned4(idx)) return M3_ERR_ALIGN;
+  int* status = status_word();
+  if (!status) return M3_ERR_CUDA;
+  return cuda_status(m3::launch_pages_free(pool->npages, live, n, idx, status, (cudaStream_t)stream));
+}
+
+m3_status m3_pages_compact(const m3_pages* pool, int32_t* live, int32_t* map, int32_t* order, int32_t* count,
+                           void* stream) {
+  m3_status st = check_pool(pool, 0);
+  if (st != M3_OK) return st;
+  if (!count || (pool->npages > 0 && (!live || !map || !order))) return M3_ERR_NULL;
+  if (!aligned4(live) || !aligned4(map) || !aligned4(order) || !aligned4(count)) return M3_ERR_ALIGN;
+  return cuda_status(m3::launch_pages_compact(*pool, live, map, order, count, (cudaStream_t)stream));
 }
 
 m3_status m3_selftest_wait(uint64_t limit_ns, void* stream) {

@@ -1,0 +1,509 @@
+// m3_linattn.cu -- linear attention with a decay per head: the recurrent core for every type and
+// size (m3_linattn.cuh), the sum over a group's heads, and the one-token step.
+//
+// The core walks a sequence token by token with the state in registers: a thread holds 16 rows x
+// 4 columns of S as packed fp32 row pairs (f32x2), so a token costs three packed operations per two
+// state elements (k v, the decayed update, the readout) and the operand rows come from shared
+// memory as broadcast 128-bit loads.  LN = KD / 16 lanes share a column, their readouts are summed
+// by a shuffle reduce-scatter.  It is bound by the fp32 pipe: 6 KD VD flops a token and head.
+// Few sequences are cut into segments: every segment but the last is walked from a zero start (MODE 1)
+// and leaves its end state; the full pass folds the earlier segments' states into its entering state.
+//
+// g itself is rounded to fp32, and a product of d of them is off by up to d 2^-25: every 16 tokens
+// the state is multiplied by e^{16 log_decay} / g^16, taken in 64 bits, which leaves at most the
+// rounding of 16 factors.
+#include "m3_linattn.cuh"
+#include "m3_ptx.cuh"
+
+namespace m3 {
+namespace {
+
+constexpr int kTB = 16;       // tokens staged at once
+constexpr int kLaWarps = 4;
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four consecutive values of a staged row.
+template <bool BF16>
+__device__ __forceinline__ float4 row4(const void* p, int i) {
+  if constexpr (BF16) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
+  } else {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  }
+}
+
+// Tokens of segment m: [lo, hi) of the padded sequence, and how many of them are valid.
+struct SegSpan {
+  int64_t lo, hi, ta, tb;
+};
+__device__ __forceinline__ SegSpan la_span(const LaCore& a, int m, int64_t len) {
+  SegSpan s;
+  const int64_t p0 = (int64_t)m * a.seg_tok, p1 = p0 + a.seg_tok < a.L ? p0 + a.seg_tok : a.L;
+  s.lo = a.rev ? a.L - p1 : p0;
+  s.hi = a.rev ? a.L - p0 : p1;
+  if (s.hi < s.lo) s.hi = s.lo;
+  s.ta = s.lo < len ? s.lo : len;
+  s.tb = s.hi < len ? s.hi : len;
+  return s;
+}
+
+template <bool BF16, bool OUT_F32, int LN, int MODE>
+__global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, int coltiles) {
+  constexpr bool FULL = MODE == 0;
+  constexpr int KDP = 16 * LN, CPW = 128 / LN, COLS = kLaWarps * CPW, E = BF16 ? 2 : 4;
+  using T = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+  constexpr int kRow = KDP, kBuf = kTB * (2 * KDP + COLS);  // q, k, v of a token block, elements
+  extern __shared__ __align__(16) uint8_t sm[];
+  T* buf = reinterpret_cast<T*>(sm);                              // [2][kBuf]
+  float* ybuf = reinterpret_cast<float*>(sm + 2 * kBuf * E);      // [kTB][COLS]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ln = lane % LN;
+  int64_t blk = blockIdx.x;
+  const int ct = (int)(blk % coltiles);
+  blk /= coltiles;
+  const int nseg_grid = FULL ? a.nseg : a.nseg - 1;
+  const int seg = (int)(blk % nseg_grid);
+  const int64_t bh = blk / nseg_grid;
+  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  const int c0 = ct * COLS;                            // first column of the block
+  const int cb = warp * CPW + (lane / LN) * 4;         // first column of the thread, within the block
+  const int ncol = a.VD - c0 < COLS ? a.VD - c0 : COLS;
+  const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
+  const int64_t len = page < 0 ? 0 : la_len(a, bi);
+  const SegSpan sp = la_span(a, seg, len);
+  const float ld = a.log_decay[h];
+  const float g = (float)la_pow(ld, 1);
+  float corr = 1.0f;
+  {
+    double gp = (double)g;
+#pragma unroll
+    for (int i = 1; i < kTB; i *= 2) gp *= gp;
+    if (gp > 1e-30) corr = (float)(la_pow(ld, kTB) / gp);
+  }
+
+  // ---- the state entering the segment: rows 4 (ln + LN j) + e as pairs, columns cb..cb+3
+  uint64_t S[8][4];
+  auto row_of = [&](int rp) { return 4 * (ln + LN * (rp >> 1)) + 2 * (rp & 1); };
+  auto slot = [&](int s) { return a.ws + (bh * a.nseg + s) * (int64_t)a.KD * a.VD; };
+  const int64_t sbase = (page * a.H + h) * (int64_t)a.KD * a.VD;
+#pragma unroll
+  for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) S[rp][c] = 0;
+  const bool has_col = cb < ncol;  // columns come in fours: VD is a multiple of 8
+  if (has_col && page >= 0) {
+    if (seg == 0 || !FULL) {
+      const bool from_ws = FULL && a.nseg > 1;
+      if (seg == 0 && (from_ws || a.s_in)) {
+        const float* src = from_ws ? slot(0) : a.s_in + sbase;
+        const int64_t si = from_ws ? a.VD : a.s_i, sj = from_ws ? 1 : a.s_j;
+#pragma unroll
+        for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = row_of(rp);
+            if (i < a.KD) S[rp][c] = f2(src[i * si + (c0 + cb + c) * sj], src[(i + 1) * si + (c0 + cb + c) * sj]);
+          }
+      }
+      if (!FULL && seg == 0) {
+        float* w = slot(0);
+#pragma unroll
+        for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = row_of(rp);
+            float lo, hi;
+            f2_split(S[rp][c], lo, hi);
+            if (i < a.KD) {
+              w[(int64_t)i * a.VD + c0 + cb + c] = lo;
+              w[(int64_t)(i + 1) * a.VD + c0 + cb + c] = hi;
+            }
+          }
+      }
+    } else {
+      for (int m = 0; m < seg; ++m) {
+        const SegSpan s = la_span(a, m, len);
+        // (against time, the sequence's first token takes the incoming state undecayed)
+        const int64_t undecayed = a.rev && s.tb == len && s.tb > s.ta;
+        const float f = (float)la_pow(ld, s.tb - s.ta - undecayed);
+        const float* z = slot(m + 1);
+#pragma unroll
+        for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = row_of(rp);
+            if (i < a.KD)
+              S[rp][c] = f2_fma(S[rp][c], f2(f, f),
+                                f2(z[(int64_t)i * a.VD + c0 + cb + c], z[(int64_t)(i + 1) * a.VD + c0 + cb + c]));
+          }
+      }
+    }
+  }
+
+  // ---- token blocks, in processing order; padding rows and columns of the buffers stay zero
+  for (int i = tid; i < 2 * kBuf * E / 16; i += 32 * kLaWarps) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int64_t ntok = sp.tb - sp.ta;
+  const int64_t nblk = (ntok + kTB - 1) / kTB;
+  const int gq = h / (a.H / a.hq), gk = h / (a.H / a.hk), gv = h / (a.H / a.hv);
+  // token of position i of the segment
+  auto token = [&](int64_t i) { return a.rev ? sp.tb - 1 - i : sp.ta + i; };
+  const int kc = a.KD * E / 16, vc = ncol * E / 16;  // 16-byte chunks of a row
+  auto stage = [&](int64_t blk_i, int s) {
+    const int64_t i0 = blk_i * kTB;
+    const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
+    T* bq = buf + s * kBuf;
+    T* bk = bq + kTB * kRow;
+    T* bv = bk + kTB * kRow;
+    for (int e = tid; e < nt * kc; e += 32 * kLaWarps) {
+      const int t = e / kc, ch = e % kc;
+      const int64_t row = (int64_t)bi * a.L + token(i0 + t);
+      if (FULL)
+        cp_async16(bq + t * kRow + ch * (16 / E), static_cast<const T*>(a.q) + (row * a.hq + gq) * a.KD + ch * (16 / E));
+      cp_async16(bk + t * kRow + ch * (16 / E), static_cast<const T*>(a.k) + (row * a.hk + gk) * a.KD + ch * (16 / E));
+    }
+    for (int e = tid; e < nt * vc; e += 32 * kLaWarps) {
+      const int t = e / vc, ch = e % vc;
+      const int64_t row = (int64_t)bi * a.L + token(i0 + t);
+      cp_async16(bv + t * COLS + ch * (16 / E),
+                 static_cast<const T*>(a.v) + (row * a.hv + gv) * a.VD + c0 + ch * (16 / E));
+    }
+  };
+  // against time the first token of the sequence meets the incoming state undecayed
+  const bool first = a.rev && sp.tb == len;
+  if (nblk > 0) stage(0, 0);
+  cp_async_commit();
+  for (int64_t ib = 0; ib < nblk; ++ib) {
+    const int s = (int)(ib & 1);
+    if (ib + 1 < nblk) stage(ib + 1, s ^ 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    const int64_t i0 = ib * kTB;
+    const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
+    const T* bq = buf + s * kBuf;
+    const T* bk = bq + kTB * kRow;
+    const T* bv = bk + kTB * kRow;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      const float gt = (first && ib == 0 && t == 0) ? 1.0f : g;
+      const uint64_t g2 = f2(gt, gt);
+      const float4 v4 = row4<BF16>(bv + t * COLS, cb);
+      const float u = a.s_upd;
+      const uint64_t v2[4] = {f2(v4.x * u, v4.x * u), f2(v4.y * u, v4.y * u), f2(v4.z * u, v4.z * u),
+                              f2(v4.w * u, v4.w * u)};
+      uint64_t y2[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 k4 = row4<BF16>(bk + t * kRow, 4 * (ln + LN * j));
+        const uint64_t ka = f2(k4.x, k4.y), kb = f2(k4.z, k4.w);
+        uint64_t qa = 0, qb = 0;
+        if (FULL) {
+          const float4 q4 = row4<BF16>(bq + t * kRow, 4 * (ln + LN * j));
+          qa = f2(q4.x, q4.y);
+          qb = f2(q4.z, q4.w);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          S[2 * j][c] = f2_fma(S[2 * j][c], g2, f2_mul(ka, v2[c]));
+          S[2 * j + 1][c] = f2_fma(S[2 * j + 1][c], g2, f2_mul(kb, v2[c]));
+          if (FULL) {
+            y2[c] = f2_fma(qa, S[2 * j][c], y2[c]);
+            y2[c] = f2_fma(qb, S[2 * j + 1][c], y2[c]);
+          }
+        }
+      }
+      if constexpr (FULL) {
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float lo, hi;
+          f2_split(y2[c], lo, hi);
+          y[c] = lo + hi;
+        }
+        // sum over the LN lanes of a column: two halving exchanges, then plain butterflies
+        int col = 0, have = 4;
+        if constexpr (LN >= 2) {
+          const bool up = ln & (LN / 2);
+          const float s0 = up ? y[0] : y[2], s1 = up ? y[1] : y[3];
+          y[0] = (up ? y[2] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 2);
+          y[1] = (up ? y[3] : y[1]) + __shfl_xor_sync(kFull, s1, LN / 2);
+          col = up ? 2 : 0;
+          have = 2;
+        }
+        if constexpr (LN >= 4) {
+          const bool up = ln & (LN / 4);
+          const float s0 = up ? y[0] : y[1];
+          y[0] = (up ? y[1] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 4);
+          col += up ? 1 : 0;
+          have = 1;
+        }
+#pragma unroll
+        for (int o = LN / 8; o > 0; o >>= 1) y[0] += __shfl_xor_sync(kFull, y[0], o);
+        if (LN < 8 || (ln & (LN / 4 - 1)) == 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < have) ybuf[t * COLS + cb + col + c] = a.s_out * y[c];
+        }
+      }
+    }
+    if (nt == kTB) {
+      const uint64_t c2 = f2(corr, corr);
+#pragma unroll
+      for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[rp][c] = f2_mul(S[rp][c], c2);
+    }
+    __syncthreads();  // the block's readouts are complete, its operands read
+    if constexpr (FULL) {
+      for (int e = tid; e < nt * ncol; e += 32 * kLaWarps) {
+        const int t = e / ncol, c = e % ncol;
+        store_out<!OUT_F32>(a.out, (((int64_t)bi * a.L + token(i0 + t)) * a.H + h) * a.VD + c0 + c, ybuf[t * COLS + c]);
+      }
+      // ybuf is rewritten after the next block's first barrier
+    }
+  }
+  cp_async_wait<0>();
+  if constexpr (FULL) {  // tokens past the sequence's length
+    for (int64_t t = sp.tb > sp.lo ? sp.tb : sp.lo; t < sp.hi; ++t)
+      for (int c = tid; c < ncol; c += 32 * kLaWarps)
+        store_out<!OUT_F32>(a.out, (((int64_t)bi * a.L + t) * a.H + h) * a.VD + c0 + c, 0.0f);
+  }
+
+  // ---- the state left behind
+  if (!has_col || page < 0) return;
+  if (!FULL || (seg == a.nseg - 1 && a.s_fin)) {
+    float* dst = FULL ? a.s_fin + sbase : slot(seg + 1);
+    const int64_t si = FULL ? a.s_i : a.VD, sj = FULL ? a.s_j : 1;
+    const float f = FULL && a.rev && len > 0 ? g : 1.0f;  // against time: once more past the first token
+#pragma unroll
+    for (int rp = 0; rp < 8; ++rp)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int i = row_of(rp);
+        float lo, hi;
+        f2_split(S[rp][c], lo, hi);
+        if (i < a.KD) {
+          dst[i * si + (c0 + cb + c) * sj] = f * lo;
+          dst[(i + 1) * si + (c0 + cb + c) * sj] = f * hi;
+        }
+      }
+  }
+}
+
+// out (rows, G, D) = sum over the H / G heads of a group of part (rows, H, D), in head order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) la_head_sum_kernel(int64_t n4, int H, int G, int D4, const float4* part, void* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const int d = (int)(i % D4);
+  const int64_t rg = i / D4;  // (row, group)
+  const int per = H / G;
+  const float4* p = part + rg * per * D4 + d;
+  float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int k = 0; k < per; ++k) {
+    const float4 v = __ldcs(p + (int64_t)k * D4);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  if constexpr (BF16) {
+    reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  } else {
+    reinterpret_cast<float4*>(out)[i] = s;
+  }
+}
+
+// One token: S <- g S + k v^T, y = scale S^T q.  A CTA takes 32 columns of one (row, head) state:
+// eight lanes read 128 bytes of a state row, sixteen row groups share the column sums.  Bound by HBM:
+// the state is read and written once.
+constexpr int kStepCols = 32, kStepThreads = 128;
+
+template <bool BF16, int ITER>
+__global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, int tiles) {
+  __shared__ float4 part[4][8];
+  const int tid = threadIdx.x, c4 = tid & 7, rg = tid >> 3, warp = tid >> 5, lane = tid & 31;
+  int64_t blk = blockIdx.x;
+  const int tile = (int)(blk % tiles);
+  const int64_t bh = blk / tiles;
+  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  const int p0 = tile * kStepCols + 4 * c4;
+  const bool on = p0 < a.P;
+  const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
+  const int64_t yi = bh * a.P + p0;
+  if (page < 0) {
+    if (on && rg == 0)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) store_out<BF16>(a.y, yi + c, 0.0f);
+    return;
+  }
+  float* S = a.state + (page * a.H + h) * (int64_t)a.N * a.P + p0;
+  float4 s[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int n = rg + 16 * i;
+    s[i] = (on && n < a.N) ? *reinterpret_cast<const float4*>(S + (int64_t)n * a.P) : make_float4(0, 0, 0, 0);
+  }
+  const float g = (float)la_pow(a.log_decay[h], 1);
+  float v[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = on ? load_in<BF16>(a.v, yi + c) : 0.0f;
+  const int64_t kq = ((int64_t)bi * a.G + h / (a.H / a.G)) * a.N;
+  float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int n = rg + 16 * i;
+    if (n < a.N) {
+      const float k = load_in<BF16>(a.k, kq + n), q = load_in<BF16>(a.q, kq + n);
+      s[i].x = fmaf(g, s[i].x, k * v[0]);
+      s[i].y = fmaf(g, s[i].y, k * v[1]);
+      s[i].z = fmaf(g, s[i].z, k * v[2]);
+      s[i].w = fmaf(g, s[i].w, k * v[3]);
+      if (on) *reinterpret_cast<float4*>(S + (int64_t)n * a.P) = s[i];
+      y.x = fmaf(q, s[i].x, y.x);
+      y.y = fmaf(q, s[i].y, y.y);
+      y.z = fmaf(q, s[i].z, y.z);
+      y.w = fmaf(q, s[i].w, y.w);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    y.x += __shfl_xor_sync(kFull, y.x, o);
+    y.y += __shfl_xor_sync(kFull, y.y, o);
+    y.z += __shfl_xor_sync(kFull, y.z, o);
+    y.w += __shfl_xor_sync(kFull, y.w, o);
+  }
+  if (lane < 8) part[warp][lane] = y;
+  __syncthreads();
+  if (tid < 8 && on) {
+    float o[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float4 f = part[w][tid];
+      o[0] += f.x;
+      o[1] += f.y;
+      o[2] += f.z;
+      o[3] += f.w;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) store_out<BF16>(a.y, yi + c, a.scale * o[c]);
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+int lanes_of(int KD) {
+  int ln = 1;
+  while (16 * ln < KD) ln *= 2;
+  return ln;
+}
+
+int cols_of(int KD) { return kLaWarps * 128 / lanes_of(KD); }
+
+// Segments of a sequence: enough CTAs for three per SM (about what the registers allow), each at
+// least 64 tokens long so that the walk outweighs reading the earlier segments' states.
+void plan_core(LaCore* a) {
+  const int64_t units = a->b * a->H * ((a->VD + cols_of(a->KD) - 1) / cols_of(a->KD));
+  int64_t nseg = units > 0 ? (int64_t)sm_count() * 3 / units : 1;
+  const int64_t most = a->L / 64;
+  if (nseg > most) nseg = most;
+  if (nseg > 64) nseg = 64;
+  if (nseg < 2) nseg = 1;
+  a->seg_tok = (a->L + nseg - 1) / nseg;
+  if (a->seg_tok < 1) a->seg_tok = 1;
+  a->nseg = (int)(a->L > 0 ? (a->L + a->seg_tok - 1) / a->seg_tok : 1);
+}
+
+template <bool BF16, bool OUT_F32, int LN, int MODE>
+cudaError_t launch_core_cfg(const LaCore& a, cudaStream_t stream) {
+  constexpr int KDP = 16 * LN, COLS = kLaWarps * 128 / LN;
+  constexpr int bytes = 2 * kTB * (2 * KDP + COLS) * (BF16 ? 2 : 4) + kTB * COLS * 4;
+  static SmemAttr attr;
+  auto k = la_core_kernel<BF16, OUT_F32, LN, MODE>;
+  const cudaError_t e = attr.ensure(k, bytes);
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.VD + COLS - 1) / COLS;
+  const int64_t grid = a.b * a.H * tiles * (MODE == 0 ? a.nseg : a.nseg - 1);
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  k<<<(unsigned)grid, 32 * kLaWarps, bytes, stream>>>(a, tiles);
+  return cudaGetLastError();
+}
+
+template <bool BF16, bool OUT_F32, int LN>
+cudaError_t launch_core_ln(const LaCore& a, cudaStream_t stream) {
+  if (a.nseg > 1) {
+    const cudaError_t e = launch_core_cfg<BF16, BF16 ? false : true, LN, 1>(a, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_core_cfg<BF16, OUT_F32, LN, 0>(a, stream);
+}
+
+template <bool BF16, bool OUT_F32>
+cudaError_t launch_core_type(const LaCore& a, cudaStream_t stream) {
+  switch (lanes_of(a.KD)) {
+    case 1: return launch_core_ln<BF16, OUT_F32, 1>(a, stream);
+    case 2: return launch_core_ln<BF16, OUT_F32, 2>(a, stream);
+    case 4: return launch_core_ln<BF16, OUT_F32, 4>(a, stream);
+    case 8: return launch_core_ln<BF16, OUT_F32, 8>(a, stream);
+    default: return launch_core_ln<BF16, OUT_F32, 16>(a, stream);
+  }
+}
+
+template <int ITER>
+cudaError_t launch_step_iter(const LaStep& a, cudaStream_t stream) {
+  const int tiles = (a.P + kStepCols - 1) / kStepCols;
+  const int64_t grid = a.b * a.H * tiles;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (a.bf16) la_step_kernel<true, ITER><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
+  else la_step_kernel<false, ITER><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t la_core_ws_bytes(const LaCore& a0) {
+  LaCore a = a0;
+  plan_core(&a);
+  return a.nseg > 1 ? sizeof(float) * (size_t)(a.b * a.H) * a.nseg * a.KD * a.VD : 0;
+}
+
+cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  plan_core(&a);
+  if (la_core_ws_bytes(a) > ws_bytes) return cudaErrorInvalidValue;
+  a.ws = static_cast<float*>(ws);
+  if (!a.bf16) return launch_core_type<false, true>(a, stream);
+  return a.out_f32 ? launch_core_type<true, true>(a, stream) : launch_core_type<true, false>(a, stream);
+}
+
+cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
+                               cudaStream_t stream) {
+  const int64_t n4 = rows * G * (D / 4);
+  if (n4 == 0) return cudaSuccess;
+  const int64_t grid = (n4 + 255) / 256;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const float4* p = reinterpret_cast<const float4*>(part);
+  if (bf16) la_head_sum_kernel<true><<<(unsigned)grid, 256, 0, stream>>>(n4, H, G, D / 4, p, out);
+  else la_head_sum_kernel<false><<<(unsigned)grid, 256, 0, stream>>>(n4, H, G, D / 4, p, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_la_step(const LaStep& a, cudaStream_t stream) {
+  if (a.N <= 64) return launch_step_iter<4>(a, stream);
+  if (a.N <= 128) return launch_step_iter<8>(a, stream);
+  return launch_step_iter<16>(a, stream);
+}
+
+}  // namespace m3

@@ -1,0 +1,98 @@
+// m3_linattn.cuh -- linear attention with a decay per head: what its kernels share.
+//
+// One operator serves the forward pass and all three gradients.  Per (batch, head), over the
+// tokens in time order (rev = 0) or against it (rev = 1), with g = e^{log_decay},
+//   S <- g S + s_upd k_t v_t^T            (KD x VD, fp32)
+//   out_t = s_out S^T q_t
+// forward:  y  = (q, k, v) in time order,  S from state_in, left in state_out
+// gradients: dq = (dy, v, k) in time order, S^T from state_in
+//            dk = (v, dy, q) against time,  from dstate_out^T
+//            dv = (k, q, dy) against time,  from dstate_out, left in dstate_in
+// Against time the incoming state meets the last token undecayed (dL/dS_{L-1} includes
+// dstate_out itself) and the state left behind is decayed once more (S_0 = g S_{-1} + ...).
+#pragma once
+
+#include "m3_common.cuh"
+
+namespace m3 {
+
+struct LaCore {
+  int64_t b, L;
+  int H, KD, VD;
+  const void *q, *k, *v;  // (b, L, hq | hk | hv, KD | KD | VD); head h of the pass reads h / (H / hx)
+  int hq, hk, hv;
+  int bf16;               // operands bf16 (else fp32)
+  int out_f32;            // out fp32 (else bf16)
+  void* out;              // (b, L, H, VD)
+  int rev;
+  float s_upd, s_out;
+  const float* log_decay;  // (H)
+  const int32_t* lens;     // (b) or null
+  const int32_t* pages;    // (b) or null: the state row of each batch row
+  int64_t npages;
+  const float* s_in;       // state row + head * KD * VD + i * s_i + j * s_j (key index i, value index j); may be null
+  float* s_fin;            // the same layout; may be null, may be s_in
+  int64_t s_i, s_j;
+  int nseg;                // segments of a sequence walked in parallel
+  int64_t seg_tok;         // tokens of a segment (in processing order)
+  float* ws;               // (b * H, nseg, KD, VD) when nseg > 1: slot 0 the incoming state, slot m + 1
+                           // the end state of segment m from a zero start (segment 0: from slot 0)
+  int* status;
+};
+
+// Tokens of batch row bi that are read.
+__device__ __forceinline__ int64_t la_len(const LaCore& a, int bi) {
+  if (!a.lens) return a.L;
+  const int64_t n = a.lens[bi];
+  return n < 0 ? 0 : n > a.L ? a.L : n;
+}
+// g^e for a whole exponent e >= 0, rounded once to fp32: computed in 64 bits, so that distant tokens keep
+// their weight to fp32 accuracy.  g = 0 (log_decay = -inf) keeps g^0 = 1.
+__device__ __forceinline__ double la_pow(float log_decay, int64_t e) {
+  return e <= 0 ? 1.0 : exp((double)log_decay * (double)e);
+}
+// The state row of batch row bi, or -1 for a row without one: a negative page (padding), a page past the
+// pool or a page that an earlier row of the batch holds already (both recorded in the status word).
+// Every thread of the block calls it; the same answer goes to all of them.
+__device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t npages, int bi, int* status) {
+  if (!pages) return bi;
+  const int p = pages[bi];
+  if (p < 0) return -1;
+  int bad = p >= npages;
+  for (int j = threadIdx.x; j < bi; j += blockDim.x) bad |= pages[j] == p;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(status, M3_ERR_STATE);
+    return -1;
+  }
+  return p;
+}
+
+// Launchers.
+size_t la_core_ws_bytes(const LaCore& a);  // scratch of the pass (plans its segments)
+cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream);
+cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
+                               cudaStream_t stream);
+struct LaStep {
+  int64_t b;
+  int H, G, N, P, bf16;
+  const void *q, *k, *v;
+  const float* log_decay;
+  float scale;
+  float* state;
+  int64_t npages;
+  const int32_t* pages;
+  void* y;
+  int* status;
+};
+cudaError_t launch_la_step(const LaStep& a, cudaStream_t stream);
+
+cudaError_t launch_pages_copy(const m3_pages& pg, int64_t n, const int32_t* src, const int32_t* dst, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_fork(const m3_pages& pg, int32_t* live, int64_t n, const int32_t* src, int32_t* dst,
+                              int* status, cudaStream_t stream);
+cudaError_t launch_pages_free(int64_t npages, int32_t* live, int64_t n, const int32_t* idx, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_compact(const m3_pages& pg, int32_t* live, int32_t* map, int32_t* order, int32_t* count,
+                                 cudaStream_t stream);
+
+}  // namespace m3

@@ -38,11 +38,21 @@ class Dims(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+PAGES_MAX_BUF = 64
+
+
+class PagesStruct(ctypes.Structure):
+    """m3_pages: the buffers of a pool of states."""
+    _fields_ = [("npages", ctypes.c_int32), ("nbuf", ctypes.c_int32), ("base", ctypes.c_void_p * PAGES_MAX_BUF),
+                ("bytes", ctypes.c_int64 * PAGES_MAX_BUF)]
+
+
 _lib = None
 
 # Every symbol include/m3.h declares, with (restype, argtypes).
 _VP, _SZ, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _DP = ctypes.POINTER(Dims)
+_PP = ctypes.POINTER(PagesStruct)
 SIGNATURES = {
     "m3_state_bytes": (_I, [_DP, ctypes.POINTER(_SZ)]),
     "m3_state_alloc": (_I, [_DP, _VP, ctypes.POINTER(_VP)]),
@@ -62,6 +72,15 @@ SIGNATURES = {
     "m3_scan_summary_workspace_size": (_I, [_DP, ctypes.POINTER(_SZ)]),
     "m3_scan_summary": (_I, [_DP] + [_VP] * 14 + [_VP, _SZ, _VP]),
     "m3_state_fold": (_I, [_DP, ctypes.c_int32] + [_VP] * 8 + [_VP, _VP]),
+    "m3_linattn_workspace_size": (_I, [_DP, ctypes.POINTER(_SZ)]),
+    "m3_linattn_fwd": (_I, [_DP] + [_VP] * 4 + [ctypes.c_float] + [_VP] * 3 + [ctypes.c_int64] + [_VP] * 3 + [_SZ, _VP]),
+    "m3_linattn_step": (_I, [_DP] + [_VP] * 4 + [ctypes.c_float, _VP, ctypes.c_int64] + [_VP] * 3),
+    "m3_linattn_bwd_workspace_size": (_I, [_DP, ctypes.POINTER(_SZ)]),
+    "m3_linattn_bwd": (_I, [_DP] + [_VP] * 4 + [ctypes.c_float] + [_VP] * 9 + [_SZ, _VP]),
+    "m3_pages_copy": (_I, [_PP, ctypes.c_int64] + [_VP] * 3),
+    "m3_pages_fork": (_I, [_PP, _VP, ctypes.c_int64] + [_VP] * 3),
+    "m3_pages_free": (_I, [_PP, _VP, ctypes.c_int64] + [_VP] * 2),
+    "m3_pages_compact": (_I, [_PP] + [_VP] * 5),
     "m3_check": (_I, [_VP]),
     "m3_selftest_wait": (_I, [ctypes.c_uint64, _VP]),
     "m3_status_str": (ctypes.c_char_p, [_I]),
@@ -276,6 +295,235 @@ def scan_backward(dims: Dims, dev: dict, state0: State, dy, dh_final=None, strea
     ws = torch.empty(max(n, 16), dtype=torch.uint8, device=d)
     m3_scan_bwd(dims, *[dev[k] for k in _OPERANDS], state0, dy, dh_final, out, workspace=ws, stream=stream)
     return out
+
+
+def _on_stream(device, stream):
+    """Context in which a call on tensors of `device` runs: that device current and `stream` (or the
+    device's current stream) the one that allocations and launches go to."""
+    import contextlib
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(stream)  # also makes the stream's device current
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _expect(what, name, t, shape, dtype, device):
+    if t.device != device or device.type != "cuda":
+        raise M3Error(-1, f"{what}: {name} is on {t.device}, expected the CUDA device of the other tensors")
+    if t.dtype != dtype:
+        raise M3Error(-2, f"{what}: {name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise M3Error(-1, f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise M3Error(-1, f"{what}: {name} is not contiguous")
+
+
+def _la_dims(what, q, k, v, log_decay, token):
+    """Dims of a linear attention call from its tensors, after their checks (token: no L axis)."""
+    import torch
+    if q.dim() != (3 if token else 4) or v.dim() != q.dim():
+        raise M3Error(-1, f"{what}: q has {q.dim()} and v {v.dim()} dimensions, expected {3 if token else 4}")
+    if q.dtype == torch.bfloat16:
+        dt = M3_BF16
+    elif q.dtype == torch.float32:
+        dt = M3_F32
+    else:
+        raise M3Error(-2, f"{what}: q is {q.dtype}, expected bfloat16 or float32")
+    b, G, N = q.shape[0], q.shape[-2], q.shape[-1]
+    H, P = v.shape[-2:]
+    L = 1 if token else q.shape[1]
+    dev = q.device
+    _expect(what, "q", q, q.shape, q.dtype, dev)
+    _expect(what, "k", k, q.shape, q.dtype, dev)
+    _expect(what, "v", v, (b, H, P) if token else (b, L, H, P), q.dtype, dev)
+    _expect(what, "log_decay", log_decay, (H,), torch.float32, dev)
+    return Dims(b, L, H, P, N, 1, G, 0, dt, 0)
+
+
+def _la_rows(what, dims, state, pages, device):
+    """Rows of the state pool a call works on, after the checks of state and pages."""
+    import torch
+    rows = dims.b if pages is None else state.shape[0]
+    _expect(what, "state", state, (rows, dims.H, dims.N, dims.P), torch.float32, device)
+    if pages is not None:
+        _expect(what, "pages", pages, (dims.b,), torch.int32, device)
+    return rows
+
+
+def m3_linattn_workspace_size(dims: Dims) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().m3_linattn_workspace_size(ctypes.byref(dims), ctypes.byref(n)), "m3_linattn_workspace_size")
+    return n.value
+
+
+def m3_linattn_fwd(dims: Dims, q, k, v, log_decay, scale, lens, state_in, state_out, npages, pages, y,
+                   workspace=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().m3_linattn_fwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), scale, _ptr(lens),
+                                _ptr(state_in), _ptr(state_out), npages, _ptr(pages), _ptr(y), _ptr(workspace),
+                                ws_bytes, _stream(stream)), "m3_linattn_fwd")
+
+
+def m3_linattn_step(dims: Dims, q_t, k_t, v_t, log_decay, scale, state, npages, pages, y_t, stream=None):
+    _check(lib().m3_linattn_step(ctypes.byref(dims), _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(log_decay), scale,
+                                 _ptr(state), npages, _ptr(pages), _ptr(y_t), _stream(stream)), "m3_linattn_step")
+
+
+def m3_linattn_bwd_workspace_size(dims: Dims) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().m3_linattn_bwd_workspace_size(ctypes.byref(dims), ctypes.byref(n)), "m3_linattn_bwd_workspace_size")
+    return n.value
+
+
+def m3_linattn_bwd(dims: Dims, q, k, v, log_decay, scale, lens, state_in, dy, dstate_out, dq, dk, dv, dstate_in,
+                   workspace=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().m3_linattn_bwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), scale, _ptr(lens),
+                                _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv),
+                                _ptr(dstate_in), _ptr(workspace), ws_bytes, _stream(stream)), "m3_linattn_bwd")
+
+
+def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y=None, workspace=None, stream=None):
+    """Linear attention with a decay per head over a batch of sequences (m3_linattn_fwd).
+
+    q, k (b, L, G, N), v (b, L, H, P) bf16 or fp32, G dividing H; log_decay (H) fp32; scale: N ** -0.5
+    if not given; lens (b) int32: the lengths of a padded batch.  state (b, H, N, P) fp32, updated in
+    place, or with pages (b) int32 the rows of a pool (npages, H, N, P); without it the sequences are
+    fresh.  Returns (y, state)."""
+    import torch
+    what = "linattn"
+    dims = _la_dims(what, q, k, v, log_decay, False)
+    dev = q.device
+    if lens is not None:
+        _expect(what, "lens", lens, (dims.b,), torch.int32, dev)
+    if pages is not None and state is None:
+        raise M3Error(-4, f"{what}: pages need a state pool")
+    rows = dims.b if state is None else _la_rows(what, dims, state, pages, dev)
+    if y is not None:
+        _expect(what, "y", y, v.shape, v.dtype, dev)
+    with _on_stream(dev, stream):
+        out = state if state is not None else torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32,
+                                                          device=dev)
+        if y is None:
+            y = torch.empty_like(v)
+        if workspace is None:
+            n = m3_linattn_workspace_size(dims)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        m3_linattn_fwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state, out, rows,
+                       pages, y, workspace)
+    return y, out
+
+
+def linattn_step(q, k, v, log_decay, state, scale=None, pages=None, y=None, stream=None):
+    """One token of every sequence (m3_linattn_step): q, k (b, G, N), v (b, H, P); state and pages as
+    for linattn, updated in place.  Returns y (b, H, P)."""
+    import torch
+    what = "linattn_step"
+    dims = _la_dims(what, q, k, v, log_decay, True)
+    rows = _la_rows(what, dims, state, pages, q.device)
+    if y is not None:
+        _expect(what, "y", y, v.shape, v.dtype, q.device)
+    with _on_stream(q.device, stream):
+        if y is None:
+            y = torch.empty_like(v)
+        m3_linattn_step(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, state, rows, pages, y)
+    return y
+
+
+def linattn_backward(q, k, v, log_decay, dy, scale=None, lens=None, state0=None, dstate=None, stream=None):
+    """Gradients of linattn (m3_linattn_bwd): dy like v; state0 the states the sequences started from
+    and dstate the gradient of the ones they ended in, (b, H, N, P) fp32 or None (zero).  Returns
+    {"dq", "dk", "dv", "dstate0"}."""
+    import torch
+    what = "linattn_backward"
+    dims = _la_dims(what, q, k, v, log_decay, False)
+    dev = q.device
+    _expect(what, "dy", dy, v.shape, v.dtype, dev)
+    if lens is not None:
+        _expect(what, "lens", lens, (dims.b,), torch.int32, dev)
+    for name, t in (("state0", state0), ("dstate", dstate)):
+        if t is not None:
+            _expect(what, name, t, (dims.b, dims.H, dims.N, dims.P), torch.float32, dev)
+    with _on_stream(dev, stream):
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+               "dstate0": torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)}
+        n = m3_linattn_bwd_workspace_size(dims)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        m3_linattn_bwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state0, dy, dstate,
+                       out["dq"], out["dk"], out["dv"], out["dstate0"], ws)
+    return out
+
+
+class Pages:
+    """A pool of recurrent states (m3_pages): `bufs` are the model's state buffers, contiguous tensors
+    that share their leading axis; page i is row i of all of them.  `live` (npages) int32 marks the
+    pages in use (all free if not given).  Page lists are int32 tensors on the pool's device; every
+    call is asynchronous on the current stream (or `stream`)."""
+
+    def __init__(self, bufs, live=None):
+        import torch
+        bufs = list(bufs)
+        if not 1 <= len(bufs) <= PAGES_MAX_BUF:
+            raise M3Error(-1, f"Pages: {len(bufs)} buffers, expected 1 to {PAGES_MAX_BUF}")
+        self.device = bufs[0].device
+        self.npages = bufs[0].shape[0] if bufs[0].dim() else 0
+        s = PagesStruct(self.npages, len(bufs))
+        for j, t in enumerate(bufs):
+            if t.dim() < 2:
+                raise M3Error(-1, f"Pages: buffer {j} has no page axis")
+            _expect("Pages", f"buffer {j}", t, (self.npages, *t.shape[1:]), t.dtype, self.device)
+            s.base[j] = t.data_ptr()
+            s.bytes[j] = t[0].numel() * t.element_size() if self.npages else 16
+        if live is None:
+            live = torch.zeros(self.npages, dtype=torch.int32, device=self.device)
+        _expect("Pages", "live", live, (self.npages,), torch.int32, self.device)
+        self.bufs, self.live, self.struct = bufs, live, s
+
+    def _list(self, what, name, t):
+        import torch
+        if t.dim() != 1:
+            raise M3Error(-1, f"{what}: {name} has shape {tuple(t.shape)}, expected one axis")
+        _expect(what, name, t, t.shape, torch.int32, self.device)
+        return t.shape[0]
+
+    def copy(self, src, dst, stream=None):
+        """Page dst[i] becomes a copy of page src[i], in list order (m3_pages_copy)."""
+        n = self._list("Pages.copy", "src", src)
+        if self._list("Pages.copy", "dst", dst) != n:
+            raise M3Error(-1, "Pages.copy: src and dst have different lengths")
+        with _on_stream(self.device, stream):
+            _check(lib().m3_pages_copy(ctypes.byref(self.struct), n, _ptr(src), _ptr(dst), _stream()), "m3_pages_copy")
+
+    def fork(self, src, stream=None):
+        """Take a free page for each entry and make it a copy of page src[i], or all zero where src[i]
+        is negative (m3_pages_fork).  Returns the pages taken, (n) int32."""
+        import torch
+        n = self._list("Pages.fork", "src", src)
+        with _on_stream(self.device, stream):
+            dst = torch.empty_like(src)
+            _check(lib().m3_pages_fork(ctypes.byref(self.struct), _ptr(self.live), n, _ptr(src), _ptr(dst), _stream()),
+                   "m3_pages_fork")
+        return dst
+
+    def free(self, idx, stream=None):
+        """The pages idx become free (m3_pages_free)."""
+        n = self._list("Pages.free", "idx", idx)
+        with _on_stream(self.device, stream):
+            _check(lib().m3_pages_free(ctypes.byref(self.struct), _ptr(self.live), n, _ptr(idx), _stream()),
+                   "m3_pages_free")
+
+    def compact(self, stream=None):
+        """Move the live pages to the front, in order (m3_pages_compact).  Returns (map, count): map
+        (npages) int32 says where each page went (-1: it was free), count (1) int32 how many are live."""
+        import torch
+        with _on_stream(self.device, stream):
+            out = torch.empty((2 * self.npages + 2,), dtype=torch.int32, device=self.device)
+            where, order, count = out[:self.npages], out[self.npages:2 * self.npages], out[2 * self.npages:]
+            _check(lib().m3_pages_compact(ctypes.byref(self.struct), _ptr(self.live), _ptr(where), _ptr(order),
+                                          _ptr(count), _stream()), "m3_pages_compact")
+        return where, count[:1]
 
 
 def m3_check(stream=None) -> int:
