@@ -308,7 +308,11 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  *     its outputs are zero and no state is touched.  So does a page past the pool, and a page that
  *     an earlier row of the batch holds already; both also leave M3_ERR_STATE for m3_check.
  * lens and pages need 4-byte alignment only.  Outputs must not overlap inputs.
- * Precision: fp32 throughout; y is rounded once to dims->dtype.
+ * Precision: fp32 throughout for fp32 tensors, for sizes outside the tensor-core tiles and in the
+ * step.  With bf16 tensors and N, P in {64, 128} the products of m3_linattn_fwd and m3_linattn_bwd
+ * run on the tensor cores with fp32 accumulation: the weighted scores and the copy of the state
+ * that q meets are rounded to bf16; the state itself stays fp32 (its updates enter as three bf16
+ * parts, 24 bits).
  */
 
 /* Scratch bytes m3_linattn_fwd needs for these dims (0 when it needs none). */

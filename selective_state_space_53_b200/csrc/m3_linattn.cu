@@ -416,6 +416,7 @@ int cols_of(int KD) { return kLaWarps * 128 / lanes_of(KD); }
 // Segments of a sequence: enough CTAs for three per SM (about what the registers allow), each at
 // least 64 tokens long so that the walk outweighs reading the earlier segments' states.
 void plan_core(LaCore* a) {
+  if (la_tc_supported(*a)) return la_tc_plan(a, sm_count());
   const int64_t units = a->b * a->H * ((a->VD + cols_of(a->KD) - 1) / cols_of(a->KD));
   int64_t nseg = units > 0 ? (int64_t)sm_count() * 3 / units : 1;
   const int64_t most = a->L / 64;
@@ -484,6 +485,7 @@ cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t str
   plan_core(&a);
   if (la_core_ws_bytes(a) > ws_bytes) return cudaErrorInvalidValue;
   a.ws = static_cast<float*>(ws);
+  if (la_tc_supported(a)) return launch_la_tc(a, stream);
   if (!a.bf16) return launch_core_type<false, true>(a, stream);
   return a.out_f32 ? launch_core_type<true, true>(a, stream) : launch_core_type<true, false>(a, stream);
 }

@@ -69,6 +69,9 @@ __device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t n
 
 // Launchers.
 size_t la_core_ws_bytes(const LaCore& a);  // scratch of the pass (plans its segments)
+bool la_tc_supported(const LaCore& a);     // the tensor-core form takes this pass
+void la_tc_plan(LaCore* a, int sms);
+cudaError_t launch_la_tc(const LaCore& a, cudaStream_t stream);  // planned, scratch in a.ws
 cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream);
 cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
                                cudaStream_t stream);
