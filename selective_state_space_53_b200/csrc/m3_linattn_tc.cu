@@ -17,18 +17,21 @@
 //
 // Roundings: A' and the copy of S that q meets are bf16 (each moves the result by less than its own
 // final rounding to bf16 does).  The state is an fp32 result, so its update must not lose bits: the
-// weighted v enters as three bf16 parts (hi + mid + lo hold 24 bits) side by side as N = 192 columns
+// weighted v enters as three bf16 parts (8 bits each: all 24 of the product) side by side as N = 192 columns
 // of one product, so k is read once for all three, and a^128 is a two-float constant.
 //
-// Warp roles (20 warps; waits are mbarrier waits that sleep in the instruction, bounded by %globaltimer):
+// Warp roles (19 warps; waits are mbarrier waits that sleep in the instruction, bounded by %globaltimer):
 //   0      producer: TMA loads of q, k, v into two stages (128-byte swizzle)
 //   1      MMA issue; tensor-memory allocation
-//   4-7    scores: A from tensor memory -> A' back to tensor memory
-//   8-11, 16-19  state and epilogue, 32 value columns each: the three parts of the update from tensor
-//          memory, S in registers, bf16(S) to shared memory; then Yi, Ya from tensor memory -> out
-//   12-15  weighted v: three bf16 parts to shared memory; zeroes rows past the sequence's length
-// MMA order per chunk i: Yi(i), update(i), Ya(i), A(i+1).  The scores of i have Yi(i) and update(i) to
-// finish in, the state of i+1 has Ya(i) and A(i+1), the weighted v of i+1 has all three.
+//   2      output store: TMA from the tile that the outputs were staged in (over the chunk's q)
+//   3-18   everything else, all sixteen warps on one task at a time, four warps (one per quarter of the
+//          rows) to 16 value columns (scores: to 32 score columns), so that a task's latency is a quarter and four warps of the
+//          same code hide each other's latencies on every scheduler.  Per chunk i: the scores A -> A'; the
+//          state after i, once the update is complete, and the weighted v of i + 1, whose buffer it has then
+//          read; bf16(S) to shared memory; the outputs of i
+// MMA order per chunk i: update(i), Yi(i), Ya(i), A(i+1), so that each SIMT task runs behind products
+// that do not need it: the scores behind update and Yi, the weighted v and the state behind Yi to A(i+1),
+// the outputs behind A(i+1) and the next update.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,14 +43,36 @@ namespace {
 
 constexpr int LQ = 128;  // tokens of a chunk
 constexpr int LV = 64;   // value columns of a CTA
-constexpr int L_PROD = 0, L_MMA = 1;
-constexpr int L_THREADS = 640;
-constexpr int LSC = LV / 2;  // state columns of one of the two state warpgroups
+constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2;
+constexpr int L_CTRL = 3;       // control warps
+constexpr int L_THREADS = 608;  // 19 warps: 104 registers a thread
+constexpr int L_SIMT = 16;     // warps of the SIMT tasks
+constexpr int LSC = LV / 4;    // value columns of a warpgroup
 constexpr unsigned long long L_WAIT_NS = 2000000000ull;  // 2 s bound on any wait
 constexpr int LBLK = 128 * 128;                          // one 64-column block of a 128-row tile, bytes
 constexpr int L_MAXPOW = LQ + 1;
 
-enum { LB_LD = 0, LB_FREE = 2, LB_SC = 4, LB_SP, LB_ST, LB_H, LB_VT, LB_Y, LB_YE, LB_DRAIN, LNBAR };
+// Barriers (pairs: one per stage).  None can complete two phases past a waiter (a parity wait would then
+// miss one): each phase needs what the waiter does after it has seen the one before, of the same pair entry.
+enum {
+  LB_LQK = 0,  // [2] q and k of a stage landed (TMA bytes)
+  LB_LV = 2,   // [2] v landed
+  LB_FK = 4,   // [2] k free: the update read it (MMA commit)
+  LB_FQ = 6,   // [2] q free: the outputs staged over it are stored (store warp)
+  LB_FV = 8,   // [2] v free: Ya complete (MMA commit; state pass: the update)
+  LB_YW = 10,  // [2] outputs staged over q
+  LB_SC = 12,  // A complete (MMA commit)
+  LB_SP,       // A' complete
+  LB_ST,       // bf16(S) in shared memory
+  LB_H,        // the update's parts complete (MMA commit)
+  LB_HC,       // the update's parts read
+  LB_VT,       // weighted v in shared memory
+  LB_YI,       // Yi complete (MMA commit)
+  LB_Y,        // Ya complete (MMA commit)
+  LB_YE,       // Yi and Ya read
+  LB_DRAIN,    // every MMA complete
+  LNBAR
+};
 
 template <int KD>
 struct LaCfg {
@@ -56,40 +81,99 @@ struct LaCfg {
   static constexpr int OFF_VT = 2 * STAGE;         // three parts of the weighted v
   static constexpr int OFF_S = OFF_VT + 3 * LBLK;  // bf16(S), KD rows of 64
   static constexpr int OFF_POW = OFF_S + KD * 128;
-  static constexpr int OFF_BAR = OFF_POW + ((L_MAXPOW * 4 + 15) & ~15);
+  static constexpr int OFF_COL = OFF_POW + ((L_MAXPOW * 4 + 15) & ~15);  // column factors of a 32-column score block
+  static constexpr int OFF_DIAG = OFF_COL + 32 * 4;                       // scaled weights of the diagonal blocks
+  static constexpr int OFF_BAR = OFF_DIAG + 64 * 4;
   static constexpr int OFF_MISC = OFF_BAR + LNBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
-  static constexpr uint32_t TM_A = 0, TM_AP = 128, TM_YI = 192, TM_YA = 256, TM_H = 320, TM_COLS = 512;
+  static constexpr uint32_t TM_A = 0, TM_AP = 128, TM_YA = 192, TM_YI = 256, TM_H = 320, TM_COLS = 512;
   static constexpr uint32_t ID_A = idesc_bf16(128, 128, false, false);
   static constexpr uint32_t ID_Y = idesc_bf16(128, LV, false, true);
   static constexpr uint32_t ID_H = idesc_bf16(KD, 3 * LV, true, true);
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait_sleep(bar, parity, 1000000)) return true;
+// Waits.  The plain try_wait suspends the warp for a while by itself; a wait that goes on looks at the
+// abort flag and the clock only every 256 tries, so that waiting warps leave the issue slots to the others
+// (the form with a suspend-time hint and a look at the clock each time took a third of all instructions).
+__device__ __forceinline__ bool la_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __noinline__ bool la_wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_sleep(bar, parity, 1000000)) {
-    if (*abort_flag) return false;
+  for (;;) {
+    for (int k = 0; k < 256; ++k)
+      if (la_try(bar, parity)) return true;
+    if (abort_flag && *abort_flag) return false;
     if (globaltimer() - t0 > L_WAIT_NS) {
-      *abort_flag = 1;
+      if (abort_flag) *abort_flag = 1;
       return false;
     }
   }
-  return true;
 }
-__device__ __forceinline__ void la_drain(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait_sleep(bar, parity, 1000000))
-    if (globaltimer() - t0 > L_WAIT_NS) return;
+__device__ __forceinline__ bool la_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int k = 0; k < 64; ++k)
+    if (la_try(bar, parity)) return true;
+  return la_wait_long(bar, parity, abort_flag);
 }
+// Bounded by time only: drains copies and MMAs in flight before the CTA exits.
+__device__ __forceinline__ void la_drain(uint32_t bar, uint32_t parity) { la_wait_long(bar, parity, nullptr); }
+__device__ __forceinline__ float lds32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_bits(uint32_t lo, uint32_t hi) { return f2(__uint_as_float(lo), __uint_as_float(hi)); }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void la_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// MMA issue and commit by the one thread that executes them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n .reg .b32 r;\n elect.sync r|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ void mma_ss1(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts1(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void mma_commit1(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// TMA tile store from shared memory, in bulk groups.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void la_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The valid chunks of a segment, in processing order: chunk(i), i < n; chunks [z0, z1) of it lie
@@ -116,12 +200,13 @@ __device__ __forceinline__ ChunkSpan la_chunks(const LaCore& a, int seg, int64_t
 template <int KD, int MODE>
 __global__ void __launch_bounds__(L_THREADS, 1)
     la_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ LaCore a) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                 const __grid_constant__ LaCore a) {
   using C = LaCfg<KD>;
   constexpr bool FULL = MODE == 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, q4 = warp & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
   const int vtiles = a.VD / LV;
   int64_t blk = blockIdx.x;
   const int vt = (int)(blk % vtiles);
@@ -136,6 +221,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 4);
   float* pw = reinterpret_cast<float*>(sm + C::OFF_POW);
   const uint32_t sBase = smem_u32(sm);
+  auto B = [&](int k) { return sBase + C::OFF_BAR + 8 * k; };
   auto sQ = [&](int s) { return sBase + (uint32_t)(s * C::STAGE); };
   auto sK = [&](int s) { return sBase + (uint32_t)(s * C::STAGE + C::TILE_K); };
   auto sV = [&](int s) { return sBase + (uint32_t)(s * C::STAGE + 2 * C::TILE_K); };
@@ -148,22 +234,26 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   }
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar[LB_LD + s], 1);
-      mbar_init(&bar[LB_FREE + s], 1);
+      for (int k : {LB_LQK, LB_LV, LB_FK, LB_FQ, LB_FV}) mbar_init(&bar[k + s], 1);
+      mbar_init(&bar[LB_YW + s], L_SIMT);
     }
-    mbar_init(&bar[LB_SC], 1);
-    mbar_init(&bar[LB_SP], 4);
-    mbar_init(&bar[LB_ST], 8);
-    mbar_init(&bar[LB_H], 1);
-    mbar_init(&bar[LB_VT], 4);
-    mbar_init(&bar[LB_Y], 1);
-    mbar_init(&bar[LB_YE], 8);
+    for (int k : {LB_SC, LB_H, LB_YI, LB_Y}) mbar_init(&bar[k], 1);
+    for (int k : {LB_SP, LB_ST, LB_HC, LB_VT, LB_YE}) mbar_init(&bar[k], L_SIMT);
     mbar_init(&bar[LB_DRAIN], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   const float ld = a.log_decay[h];
-  if (tid < L_MAXPOW) pw[tid] = (float)la_pow(ld, tid);
+  float* colf = reinterpret_cast<float*>(sm + C::OFF_COL);
+  float* diag = reinterpret_cast<float*>(sm + C::OFF_DIAG);
+  if (tid < L_MAXPOW) {
+    const float w = (float)la_pow(ld, tid);
+    pw[tid] = w;
+    if (tid < 32) {
+      colf[a.rev ? tid : 31 - tid] = w;
+      diag[31 + tid] = diag[31 - tid] = a.s_upd * a.s_out * w;  // weight of the distance |j - 31|
+    }
+  }
   const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
   const int64_t len = page < 0 ? 0 : la_len(a, bi);
   const ChunkSpan cs = la_chunks(a, seg, len);
@@ -179,51 +269,75 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     return left < LQ ? (int)left : LQ;
   };
 
-  if (wg == 0) {
+  if (warp < L_CTRL) {
     if (warp == L_PROD) {
       // =============================================================== producer
       if (lane == 0) {
         const int gq = h / (a.H / a.hq), gk = h / (a.H / a.hk), gv = h / (a.H / a.hv);
-        uint32_t ph = 0;  // phase bits of LB_FREE
         int done = 0;
         for (int i = 0; i < n; ++i) {
-          const int s = i & 1;
-          if (i >= 2) {
-            if (!la_wait(&bar[LB_FREE + s], (ph >> s) & 1, abort_flag)) break;
-            ph ^= 1u << s;
-          }
-          const int tok = (int)(chunk(i) * LQ);
-          mbar_expect_tx(&bar[LB_LD + s], FULL ? C::STAGE : C::STAGE - C::TILE_K);
+          const int s = i & 1, tok = (int)(chunk(i) * LQ);
+          const uint32_t before = (uint32_t)(((i >> 1) & 1) ^ 1);  // phase of the stage's chunk i - 2
+          if (i >= 2 && !la_wait(B(LB_FK + s), before, abort_flag)) break;
+          mbar_expect_tx(&bar[LB_LQK + s], FULL ? 2 * C::TILE_K : C::TILE_K);
 #pragma unroll
-          for (int b = 0; b < KD / 64; ++b) {
-            if constexpr (FULL) tma_load_4d(sQ(s) + b * LBLK, &tmQ, 64 * b, gq, tok, bi, &bar[LB_LD + s]);
-            tma_load_4d(sK(s) + b * LBLK, &tmK, 64 * b, gk, tok, bi, &bar[LB_LD + s]);
+          for (int b = 0; b < KD / 64; ++b) tma_load_4d(sK(s) + b * LBLK, &tmK, 64 * b, gk, tok, bi, &bar[LB_LQK + s]);
+          if (i >= 2) la_wait(B(LB_FV + s), before, abort_flag);  // a timeout still completes the barriers
+          mbar_expect_tx(&bar[LB_LV + s], LBLK);
+          tma_load_4d(sV(s), &tmV, LV * vt, gv, tok, bi, &bar[LB_LV + s]);
+          if constexpr (FULL) {
+            if (i >= 2) la_wait(B(LB_FQ + s), before, abort_flag);
+#pragma unroll
+            for (int b = 0; b < KD / 64; ++b) tma_load_4d(sQ(s) + b * LBLK, &tmQ, 64 * b, gq, tok, bi, &bar[LB_LQK + s]);
           }
-          tma_load_4d(sV(s), &tmV, LV * vt, gv, tok, bi, &bar[LB_LD + s]);
           ++done;
         }
         // every copy issued has landed before the CTA may exit
         for (int s = 0; s < 2; ++s) {
           const int k = (done + 1 - s) / 2;  // copies into stage s
-          if (k > 0) la_drain(&bar[LB_LD + s], (uint32_t)((k - 1) & 1));
+          if (k > 0) la_drain(B(LB_LQK + s), (uint32_t)((k - 1) & 1));
+          if (k > 0) la_drain(B(LB_LV + s), (uint32_t)((k - 1) & 1));
+        }
+      }
+    } else if (warp == L_STORE) {
+      // =============================================================== output store
+      if constexpr (FULL) {
+        if (lane == 0) {
+          for (int i = 0; i < n; ++i) {
+            const int s = i & 1;
+            if (!la_wait(B(LB_YW + s), (uint32_t)((i >> 1) & 1), abort_flag)) break;
+            if (!a.out_f32) {  // tokens past L are not written
+              tma_store_4d(&tmO, sQ(s), LV * vt, h, (int)(chunk(i) * LQ), bi);
+              bulk_commit();
+              bulk_wait_read();
+            }
+            la_arrive(B(LB_FQ + s));
+          }
+          bulk_wait_all();
         }
       }
     } else if (warp == L_MMA && n > 0) {
       // =============================================================== MMA issue
-      auto kdesc = [&](uint32_t base, int k) {  // K-major operand, K-step k of 16
-        return sdesc(base + (uint32_t)(k >> 2) * LBLK + (uint32_t)(k & 3) * 32, 16, 1024);
-      };
-      auto mdesc = [&](uint32_t base, int k) { return sdesc(base + (uint32_t)k * 2048, LBLK, 1024); };  // MN-major
-      uint32_t ph_ld = 0;
-      auto scores = [&](int i) -> bool {
+      // Operand descriptors of stage 0; a stage, a block and a K-step are plain address offsets.
+      const uint64_t dQ = sdesc(sQ(0), 16, 1024), dK = sdesc(sK(0), 16, 1024);          // K-major
+      const uint64_t dKt = sdesc(sK(0), LBLK, 1024), dVm = sdesc(sV(0), LBLK, 1024);    // MN-major
+      const uint64_t dS = sdesc(sS, LBLK, 1024), dVT = sdesc(sVT, LBLK, 1024);
+      auto stage = [&](int i) { return (uint64_t)((i & 1) * (C::STAGE >> 4)); };
+      auto kstep = [](int k) { return (uint64_t)(((k >> 2) * LBLK + (k & 3) * 32) >> 4); };
+      auto mstep = [](int k) { return (uint64_t)((k * 2048) >> 4); };
+      const bool lead = elect_one();
+      auto scores = [&](int i) -> bool {  // A of chunk i
         const int s = i & 1;
-        if (!la_wait(&bar[LB_LD + s], (ph_ld >> s) & 1, abort_flag)) return false;
-        ph_ld ^= 1u << s;
+        if (!la_wait(B(LB_LQK + s), (uint32_t)((i >> 1) & 1), abort_flag)) return false;
         if constexpr (FULL) {
           tc_fence_after();
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < KD / 16; ++k) mma_ss_w(tmem + C::TM_A, kdesc(sQ(s), k), kdesc(sK(s), k), C::ID_A, k > 0);
-          mma_commit_w(&bar[LB_SC]);
+            for (int k = 0; k < KD / 16; ++k)
+              mma_ss1(tmem + C::TM_A, dQ + stage(i) + kstep(k), dK + stage(i) + kstep(k), C::ID_A, k > 0);
+            mma_commit1(&bar[LB_SC]);
+          }
+          __syncwarp();
         }
         return true;
       };
@@ -231,159 +345,74 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       for (int i = 0; ok && i < n; ++i) {
         const int s = i & 1;
         const uint32_t p = (uint32_t)(i & 1);
-        ok = la_wait(&bar[LB_ST], p, abort_flag);
-        if (FULL && ok && i > 0) ok = la_wait(&bar[LB_YE], p ^ 1, abort_flag);
+        ok = la_wait(B(LB_VT), p, abort_flag);
+        if (ok && i > 0) ok = la_wait(B(LB_HC), p ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if constexpr (FULL) {
-#pragma unroll
-          for (int k = 0; k < KD / 16; ++k) mma_ss_w(tmem + C::TM_YI, kdesc(sQ(s), k), mdesc(sS, k), C::ID_Y, k > 0);
-        }
-        ok = la_wait(&bar[LB_VT], p, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < LQ / 16; ++k) mma_ss_w(tmem + C::TM_H, mdesc(sK(s), k), mdesc(sVT, k), C::ID_H, k > 0);
-        mma_commit_w(&bar[LB_H]);
-        if constexpr (FULL) {
-          ok = la_wait(&bar[LB_SP], p, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
+        if (lead) {
 #pragma unroll
           for (int k = 0; k < LQ / 16; ++k)
-            mma_ts_w(tmem + C::TM_YA, tmem + C::TM_AP + 8 * k, mdesc(sV(s), k), C::ID_Y, k > 0);
-          mma_commit_w(&bar[LB_Y]);
+            mma_ss1(tmem + C::TM_H, dKt + stage(i) + mstep(k), dVT + mstep(k), C::ID_H, k > 0);
+          mma_commit1(&bar[LB_H]);
+          mma_commit1(&bar[LB_FK + s]);
+          if (!FULL) mma_commit1(&bar[LB_FV + s]);
         }
-        mma_commit_w(&bar[LB_FREE + s]);
+        __syncwarp();
+        if constexpr (FULL) {
+          ok = la_wait(B(LB_ST), p, abort_flag);
+          if (ok && i > 0) ok = la_wait(B(LB_YE), p ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < KD / 16; ++k)
+              mma_ss1(tmem + C::TM_YI, dQ + stage(i) + kstep(k), dS + mstep(k), C::ID_Y, k > 0);
+            mma_commit1(&bar[LB_YI]);
+          }
+          __syncwarp();
+          ok = la_wait(B(LB_SP), p, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < LQ / 16; ++k)
+              mma_ts1(tmem + C::TM_YA, tmem + C::TM_AP + 8 * k, dVm + stage(i) + mstep(k), C::ID_Y, k > 0);
+            mma_commit1(&bar[LB_Y]);
+            mma_commit1(&bar[LB_FV + s]);
+          }
+          __syncwarp();
+        }
         if (i + 1 < n) ok = scores(i + 1);
       }
       // every MMA issued has completed before tensor memory is released
-      mma_commit_w(&bar[LB_DRAIN]);
-      la_drain(&bar[LB_DRAIN], 0);
-    }
-  } else if (wg == 1) {
-    if constexpr (FULL) {
-      // =============================================================== scores
-      const float sc = a.s_upd * a.s_out;
-      uint64_t u[16];  // the columns' factors within a 32-column block
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        u[e] = a.rev ? f2(pw[2 * e], pw[2 * e + 1]) : f2(pw[31 - 2 * e], pw[30 - 2 * e]);
-      for (int i = 0; i < n; ++i) {
-        if (!la_wait(&bar[LB_SC], (uint32_t)(i & 1), abort_flag)) break;
-        tc_fence_after();
-        const int nv = valid(i);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[16];
-          const int d = a.rev ? c - q4 : q4 - c;  // blocks between the row's and the column's
-          if (d < 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          } else {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_base + C::TM_A + 32 * c, v);
-            if (d > 0) {
-              const float r = sc * pw[a.rev ? 32 * d - lane : 32 * d - 31 + lane];
-              const uint64_t r2 = f2(r, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x, y;
-                f2_split(f2_mul(f2_mul(f2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), u[e]), r2), x, y);
-                v[2 * e] = __float_as_uint(x);
-                v[2 * e + 1] = __float_as_uint(y);
-              }
-            } else {
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int dd = a.rev ? e - lane : lane - e;
-                v[e] = dd >= 0 ? __float_as_uint(__uint_as_float(v[e]) * (sc * pw[dd < 0 ? 0 : dd])) : 0u;
-              }
-            }
-            if (32 * c + 32 > nv) {  // columns past the length
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= nv) v[e] = 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = pack_bf16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          }
-          tmem_st16(tmem + lane_base + C::TM_AP + 16 * c, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) la_arrive(&bar[LB_SP]);
-      }
-    }
-  } else if (wg == 3) {
-    // =============================================================== weighted v
-    const int r = 32 * q4 + lane;  // token of the chunk
-    uint32_t ph_ld = 0;
-    for (int i = 0; i < n; ++i) {
-      const int s = i & 1;
-      if (!la_wait(&bar[LB_LD + s], (ph_ld >> s) & 1, abort_flag)) break;
-      ph_ld ^= 1u << s;
-      if (i > 0 && !la_wait(&bar[LB_H], (uint32_t)((i - 1) & 1), abort_flag)) break;  // the parts are read
-      const int nv = valid(i);
-      const uint32_t ro = (uint32_t)r * 128u;
-      if (r < nv) {
-        const float w = a.s_upd * pw[a.rev ? r + 1 : nv - 1 - r];
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t off = ro + (uint32_t)((c ^ (r & 7)) << 4);
-          float f[8];
-          unpack8(lds128(sV(s) + off), f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= w;
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint4 p = pack8(f);
-            sts128(sVT + part * LBLK + off, p);
-            if (part < 2) {
-              float g[8];
-              unpack8(p, g);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] -= g[e];  // exact
-            }
-          }
-        }
-      } else {
-        // rows past the length: zero, so that nothing found there (infinities, NaN) meets a product
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          sts128(sV(s) + ro + 16 * c, zero);
-#pragma unroll
-          for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + ro + 16 * c, zero);
-#pragma unroll
-          for (int part = 0; part < 3; ++part) sts128(sVT + part * LBLK + ro + 16 * c, zero);
-        }
-      }
-      fence_async_smem();
+      if (lead) mma_commit1(&bar[LB_DRAIN]);
       __syncwarp();
-      if (lane == 0) la_arrive(&bar[LB_VT]);
+      la_drain(B(LB_DRAIN), 0);
     }
   } else {
-    // =============================================================== state and epilogue
-    // Two warpgroups, LSC value columns each.  Per chunk: the state after it (needed by the next chunk's Yi
-    // and update) first, then the outputs of the chunk.
-    const int c0 = wg == 2 ? 0 : LSC;  // first column, within the CTA's
-    // accumulator row of this thread (M = 128: its lane; M = 64: lanes 0-15 of each quarter)
+    // =============================================================== scores, weighted v, state, outputs
+    const int w = (warp - L_CTRL) >> 2;            // value columns 16 w .. 16 w + 15, score columns 32 w .. 32 w + 31
+    const int t = 32 * q4 + lane;    // this thread's token of a chunk (scores, weighted v, outputs)
+    const uint32_t ro = (uint32_t)t * 128u;
+    // accumulator row of the state (M = 128: the lane; M = 64: lanes 0-15 of each quarter)
     const bool owner = KD == 128 || lane < 16;
-    const int row = KD == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);
-    const int64_t col = LV * vt + c0;
+    const int row = KD == 128 ? t : 16 * q4 + (lane & 15);
+    const int64_t col = LV * vt + LSC * w;
+    auto arrive = [&](int k) {
+      __syncwarp();
+      if (lane == 0) la_arrive(B(k));
+    };
+
+    // ---- the state entering the segment
     float S[LSC];
 #pragma unroll
     for (int e = 0; e < LSC; ++e) S[e] = 0.0f;
     auto slot = [&](int s) { return a.ws + ((bh * a.nseg + s) * KD + row) * (int64_t)a.VD + col; };
     const int64_t sbase = (page * a.H + h) * (int64_t)KD * a.VD + row * a.s_i + col * a.s_j;
     auto store_slot = [&](int s) {
-      float4* w = reinterpret_cast<float4*>(slot(s));
+      float4* p = reinterpret_cast<float4*>(slot(s));
 #pragma unroll
-      for (int e = 0; e < LSC / 4; ++e) w[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+      for (int e = 0; e < LSC / 4; ++e) p[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
     };
     if (owner && page >= 0) {
       if (seg == 0) {
@@ -410,88 +439,209 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         }
       }
     }
+    uint64_t S2[LSC / 2];  // the state from here on, in pairs
+#pragma unroll
+    for (int e = 0; e < LSC / 2; ++e) S2[e] = f2(S[2 * e], S[2 * e + 1]);
     auto publish = [&]() {  // bf16(S), the B operand of Yi
-      if constexpr (FULL) {
-        if (owner) {
+      if (owner) {
 #pragma unroll
-          for (int c = 0; c < LSC / 8; ++c) {
-            float f[8];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = S[8 * c + e];
-            sts128(sS + row * 128 + (((c + c0 / 8) ^ (row & 7)) << 4), pack8(f));
+          for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            f2_split(S2[4 * c + e], lo, hi);
+            o[e] = pack_bf16(lo, hi);
+          }
+          sts128(sS + row * 128 + (((c + 2 * w) ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      }
+      fence_async_smem();
+      arrive(LB_ST);
+    };
+
+    // ---- the weighted v of chunk i: three parts of this thread's 16 values; each part takes the upper 16
+    // bits of what is left, 24 bits in all
+    const int part = a.rev ? 0 : n - 1;  // the one chunk that the sequence's end may cut
+    const int nv_part = n > 0 ? valid(part) : LQ;
+    const uint32_t sPow = sBase + C::OFF_POW;
+    auto weigh = [&](int i) -> bool {
+      const int s = i & 1, nv = i == part ? nv_part : LQ;
+      if (!la_wait(B(LB_LV + s), (uint32_t)((i >> 1) & 1), abort_flag)) return false;
+      const bool in = t < nv;
+      const float wt = in ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
+      const uint64_t w2 = f2(wt, wt), minus = f2(-1.0f, -1.0f);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t off = ro + (uint32_t)(((c + 2 * w) ^ (t & 7)) << 4);
+        uint4 raw = lds128(sV(s) + off);
+        if (!in) raw = make_uint4(0, 0, 0, 0);  // past the length there may be anything
+        uint64_t f[4] = {f2_mul(f2(bf_lo(raw.x), bf_hi(raw.x)), w2), f2_mul(f2(bf_lo(raw.y), bf_hi(raw.y)), w2),
+                         f2_mul(f2(bf_lo(raw.z), bf_hi(raw.z)), w2), f2_mul(f2(bf_lo(raw.w), bf_hi(raw.w)), w2)};
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            f2_split(f[e], lo, hi);
+            o[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            if (q < 2)  // exact
+              f[e] = f2_fma(f2(__uint_as_float(__float_as_uint(lo) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(hi) & 0xffff0000u)), minus, f[e]);
+          }
+          sts128(sVT + q * LBLK + off, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      }
+      if (nv < LQ) {  // no infinity or NaN found past the length meets a product
+        if (!la_wait(B(LB_LQK + s), (uint32_t)((i >> 1) & 1), abort_flag)) return false;
+        if (t >= nv) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 2 * w; c < 2 * w + 2; ++c) {
+            sts128(sV(s) + ro + 16 * c, zero);
+#pragma unroll
+            for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + ro + 16 * c, zero);
           }
         }
-        fence_async_smem();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) la_arrive(&bar[LB_ST]);
+      fence_async_smem();
+      arrive(LB_VT);
+      return true;
     };
+
     // the decay of a full chunk as two floats: a long memory multiplies it in hundreds of times
-    const float a128_lo = (float)(la_pow(ld, LQ) - (double)pw[LQ]);
-    const int t = 32 * q4 + lane;  // token of the chunk whose outputs this thread writes
+    const float a128 = lds32(sPow + 4 * LQ), a128_lo = (float)(la_pow(ld, LQ) - (double)a128);
+    const int d = a.rev ? w - q4 : q4 - w;  // score blocks between this warp's rows and columns
+    // diagonal blocks: the weight of column e lies e words on (mirrored table), kept where bit e is set
+    const uint32_t sDg = sBase + C::OFF_DIAG + 4 * (31 - lane), sCol = sBase + C::OFF_COL;
+    const uint32_t keep = a.rev ? kFull << lane : kFull >> (31 - lane);
+    const float rowf = d > 0 ? a.s_upd * a.s_out * lds32(sPow + 4 * (a.rev ? 32 * d - lane : 32 * d - 31 + lane)) : 0.0f;
     auto out_row = [&](int64_t tok) { return (((int64_t)bi * a.L + tok) * a.H + h) * (int64_t)a.VD + col; };
     bool ok = true;
-    if (n > 0) publish();
-    for (int i = 0; i < n; ++i) {
-      ok = la_wait(&bar[LB_H], (uint32_t)(i & 1), abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      const int nv = valid(i);
-      const float ghi = pw[nv], glo = nv == LQ ? a128_lo : 0.0f;
-#pragma unroll
-      for (int c = 0; c < LSC / 8; ++c) {
-        uint32_t x[8], y[8], z[8];
-        tmem_ld8(tmem + lane_base + C::TM_H + c0 + 8 * c, x);
-        tmem_ld8(tmem + lane_base + C::TM_H + LV + c0 + 8 * c, y);
-        tmem_ld8(tmem + lane_base + C::TM_H + 2 * LV + c0 + 8 * c, z);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float hsum = __uint_as_float(x[e]) + (__uint_as_float(y[e]) + __uint_as_float(z[e]));
-          S[8 * c + e] = fmaf(ghi, S[8 * c + e], fmaf(glo, S[8 * c + e], hsum));
-        }
-      }
-      if (i + 1 < n) publish();
+    if (n > 0) {
+      if constexpr (FULL) publish();
+      ok = weigh(0);
+    }
+    for (int i = 0; ok && i < n; ++i) {
+      const int s = i & 1;
+      const uint32_t p = (uint32_t)(i & 1);
+      const int nv = i == part ? nv_part : LQ;
       if constexpr (FULL) {
-        ok = la_wait(&bar[LB_Y], (uint32_t)(i & 1), abort_flag);
+        // ---- scores: rows of this quarter, 32 columns
+        ok = la_wait(B(LB_SC), p, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const int64_t tok = chunk(i) * LQ + t;
-        const bool on = t < nv, write = tok < a.L;
-        const float f = on ? a.s_out * pw[a.rev ? nv - 1 - t : t + 1] : 0.0f;
-        const int64_t o = out_row(tok);
+        uint32_t o[16];
+        if (d < 0) {
 #pragma unroll
-        for (int c = 0; c < LSC / 16; ++c) {
-          uint32_t x[16], y[16];
-          tmem_ld16(tmem + lane_base + C::TM_YI + c0 + 16 * c, x);
-          tmem_ld16(tmem + lane_base + C::TM_YA + c0 + 16 * c, y);
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
+        } else {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_base + C::TM_A + 32 * w, v);
           tmem_wait_ld();
-          if (c == LSC / 16 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) la_arrive(&bar[LB_YE]);
+          if (d > 0) {
+            const uint64_t r2 = f2(rowf, rowf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint4 u = lds128(sCol + 16 * e);
+              float x0, x1, x2, x3;
+              f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
+              f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
+              o[2 * e] = pack_bf16(x0, x1);
+              o[2 * e + 1] = pack_bf16(x2, x3);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              // a select: what lies ahead may be infinite
+              const float x0 = __uint_as_float(v[2 * e]) * lds32(sDg + 8 * e);
+              const float x1 = __uint_as_float(v[2 * e + 1]) * lds32(sDg + 8 * e + 4);
+              o[e] = pack_bf16((keep >> (2 * e)) & 1 ? x0 : 0.0f, (keep >> (2 * e + 1)) & 1 ? x1 : 0.0f);
+            }
           }
-          float v[16];
+          if (32 * w + 32 > nv) {  // columns past the length
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            v[e] = on ? fmaf(f, __uint_as_float(x[e]), __uint_as_float(y[e])) : 0.0f;
-          if (write) {
-            if (a.out_f32) {
-              float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) + 4 * c;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) p[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            } else {
-              uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) + 2 * c;
-              p[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-              p[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]),
-                                pack_bf16(v[14], v[15]));
+            for (int e = 0; e < 16; ++e) {
+              if (32 * w + 2 * e >= nv) o[e] = 0u;
+              else if (32 * w + 2 * e + 1 >= nv) o[e] &= 0xffffu;
             }
           }
         }
+        tmem_st16(tmem + lane_base + C::TM_AP + 16 * w, o);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(LB_SP);
+      }
+      // ---- the next chunk's weighted v, once the update has read this one's; the state
+      ok = la_wait(B(LB_H), p, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const float ghi = nv == LQ ? a128 : lds32(sPow + 4 * nv), glo = nv == LQ ? a128_lo : 0.0f;
+#pragma unroll
+      for (int c = 0; c < LSC / 8; ++c) {
+        uint32_t x[8], y[8], z[8];
+        tmem_ld8(tmem + lane_base + C::TM_H + LSC * w + 8 * c, x);
+        tmem_ld8(tmem + lane_base + C::TM_H + LV + LSC * w + 8 * c, y);
+        tmem_ld8(tmem + lane_base + C::TM_H + 2 * LV + LSC * w + 8 * c, z);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t hs = f2_add(f2_bits(x[2 * e], x[2 * e + 1]),
+                                     f2_add(f2_bits(y[2 * e], y[2 * e + 1]), f2_bits(z[2 * e], z[2 * e + 1])));
+          S2[4 * c + e] = f2_fma(f2(ghi, ghi), S2[4 * c + e], f2_fma(f2(glo, glo), S2[4 * c + e], hs));
+        }
+      }
+      tc_fence_before();
+      arrive(LB_HC);
+      if (i + 1 < n && !weigh(i + 1)) break;
+      if constexpr (FULL) {
+        if (i + 1 < n) {
+          ok = la_wait(B(LB_YI), p, abort_flag);  // Yi has read the copy before
+          if (!ok) break;
+          publish();
+        }
+        // ---- outputs of the chunk
+        ok = la_wait(B(LB_Y), p, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const bool on = t < nv;
+        const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
+        uint32_t x[16], y[16];
+        tmem_ld16(tmem + lane_base + C::TM_YI + LSC * w, x);
+        tmem_ld16(tmem + lane_base + C::TM_YA + LSC * w, y);
+        tmem_wait_ld();
+        tc_fence_before();
+        arrive(LB_YE);
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          f2_split(f2_fma(f2(f, f), f2_bits(x[2 * e], x[2 * e + 1]), f2_bits(y[2 * e], y[2 * e + 1])), v[2 * e], v[2 * e + 1]);
+        if (!on) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+        }
+        if (a.out_f32) {
+          const int64_t tok = chunk(i) * LQ + t;
+          if (tok < a.L) {
+            float4* g = reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row(tok));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        } else {  // over q of the stage, which Yi was the last to read
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            sts128(sQ(s) + ro + (((c + 2 * w) ^ (t & 7)) << 4),
+                   make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                              pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7])));
+          fence_async_smem();
+        }
+        arrive(LB_YW + s);
       }
     }
-    if (ok && owner && page >= 0) {
+#pragma unroll
+    for (int e = 0; e < LSC / 2; ++e) f2_split(S2[e], S[2 * e], S[2 * e + 1]);
+    if (ok && !*abort_flag && owner && page >= 0) {
       if (!FULL) {
         store_slot(seg + 1);
       } else if (seg == a.nseg - 1 && a.s_fin) {
@@ -504,8 +654,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         const int64_t tok = j * LQ + t;
         if (tok >= a.L) continue;
         const int e = a.out_f32 ? 4 : 2;
-        uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + out_row(tok) * e);
-        for (int c = 0; c < LSC * e / 16; ++c) p[c] = make_uint4(0, 0, 0, 0);
+        uint4* g = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + out_row(tok) * e);
+        for (int c = 0; c < LSC * e / 16; ++c) g[c] = make_uint4(0, 0, 0, 0);
       }
     }
   }
@@ -547,28 +697,30 @@ bool la_map(CUtensorMap* m, const LaCore& a, const void* base, int heads, int D)
 }
 
 template <int KD, int MODE>
-cudaError_t launch_tc_mode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const LaCore& a,
-                           cudaStream_t stream) {
+cudaError_t launch_tc_mode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
+                           const LaCore& a, cudaStream_t stream) {
   static SmemAttr attr;
   auto kern = la_tc_kernel<KD, MODE>;
   const cudaError_t e = attr.ensure(kern, LaCfg<KD>::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = a.b * a.H * (a.VD / LV) * (MODE == 0 ? a.nseg : a.nseg - 1);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)grid, L_THREADS, LaCfg<KD>::SMEM, stream>>>(q, k, v, a);
+  kern<<<(unsigned)grid, L_THREADS, LaCfg<KD>::SMEM, stream>>>(q, k, v, o, a);
   return cudaGetLastError();
 }
 
 template <int KD>
 cudaError_t launch_tc_kd(const LaCore& a, cudaStream_t stream) {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   if (!la_map(&q, a, a.q, a.hq, KD) || !la_map(&k, a, a.k, a.hk, KD) || !la_map(&v, a, a.v, a.hv, a.VD))
     return cudaErrorInvalidValue;
+  if (a.out_f32) o = v;  // unused: fp32 outputs are written from registers
+  else if (!la_map(&o, a, a.out, a.H, a.VD)) return cudaErrorInvalidValue;
   if (a.nseg > 1) {
-    const cudaError_t e = launch_tc_mode<KD, 1>(q, k, v, a, stream);
+    const cudaError_t e = launch_tc_mode<KD, 1>(q, k, v, o, a, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_tc_mode<KD, 0>(q, k, v, a, stream);
+  return launch_tc_mode<KD, 0>(q, k, v, o, a, stream);
 }
 
 }  // namespace
