@@ -20,11 +20,12 @@
 // weighted v enters as three bf16 parts (8 bits each: all 24 of the product) side by side as N = 192 columns
 // of one product, so k is read once for all three, and a^128 is a two-float constant.
 //
-// Warp roles (19 warps; waits are mbarrier waits that sleep in the instruction, bounded by %globaltimer):
+// Warp roles (20 warps; every mbarrier wait is bounded by %globaltimer):
 //   0      producer: TMA loads of q, k, v into two stages (128-byte swizzle)
 //   1      MMA issue; tensor-memory allocation
 //   2      output store: TMA from the tile that the outputs were staged in (over the chunk's q)
-//   3-18   everything else, all sixteen warps on one task at a time, four warps (one per quarter of the
+//   3      signals: waits for products and copies on behalf of
+//   4-19   everything else, all sixteen warps on one task at a time, four warps (one per quarter of the
 //          rows) to 16 value columns (scores: to 32 score columns), so that a task's latency is a quarter and four warps of the
 //          same code hide each other's latencies on every scheduler.  Per chunk i: the scores A -> A'; the
 //          state after i, once the update is complete, and the weighted v of i + 1, whose buffer it has then
@@ -43,10 +44,12 @@ namespace {
 
 constexpr int LQ = 128;  // tokens of a chunk
 constexpr int LV = 64;   // value columns of a CTA
-constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2;
-constexpr int L_CTRL = 3;       // control warps
-constexpr int L_THREADS = 608;  // 19 warps: 104 registers a thread
+constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2, L_SIGNAL = 3;
+constexpr int L_CTRL = 4;       // control warps
+constexpr int L_THREADS = 640;
 constexpr int L_SIMT = 16;     // warps of the SIMT tasks
+// named barriers of the SIMT warps and the signal warp: what the SIMT warps wait for
+constexpr uint32_t LN_SC = 1, LN_H = 2, LN_YI = 3, LN_Y = 4, LN_THREADS = 32 * (L_SIMT + 1);
 constexpr int LSC = LV / 4;    // value columns of a warpgroup
 constexpr unsigned long long L_WAIT_NS = 2000000000ull;  // 2 s bound on any wait
 constexpr int LBLK = 128 * 128;                          // one 64-column block of a 128-row tile, bytes
@@ -316,6 +319,39 @@ __global__ void __launch_bounds__(L_THREADS, 1)
           bulk_wait_all();
         }
       }
+    } else if (warp == L_SIGNAL) {
+      // =============================================================== signals
+      // Waits for the products and the v copies on behalf of the SIMT warps and meets them on a named barrier,
+      // where a waiting warp takes no issue slots.  After a timeout it meets them without waiting, so that
+      // they run through their chunks (within bounds, the results void) and everyone leaves.
+      bool ok = true;
+      if (n > 0) {
+        ok = la_wait(B(LB_LV), 0, abort_flag) && la_wait(B(LB_LQK), 0, abort_flag);
+        named_bar_sync(LN_H, LN_THREADS);
+      }
+      for (int i = 0; i < n; ++i) {
+        const uint32_t p = (uint32_t)(i & 1);
+        if constexpr (FULL) {
+          ok = ok && la_wait(B(LB_SC), p, abort_flag);
+          named_bar_sync(LN_SC, LN_THREADS);
+        }
+        ok = ok && la_wait(B(LB_H), p, abort_flag);
+        if (i + 1 < n) {  // the next chunk's v, and k where the sequence's end cuts the chunk
+          const int s = (i + 1) & 1;
+          const uint32_t ps = (uint32_t)(((i + 1) >> 1) & 1);
+          ok = ok && la_wait(B(LB_LV + s), ps, abort_flag);
+          if (valid(i + 1) < LQ) ok = ok && la_wait(B(LB_LQK + s), ps, abort_flag);
+        }
+        named_bar_sync(LN_H, LN_THREADS);
+        if constexpr (FULL) {
+          if (i + 1 < n) {
+            ok = ok && la_wait(B(LB_YI), p, abort_flag);
+            named_bar_sync(LN_YI, LN_THREADS);
+          }
+          ok = ok && la_wait(B(LB_Y), p, abort_flag);
+          named_bar_sync(LN_Y, LN_THREADS);
+        }
+      }
     } else if (warp == L_MMA && n > 0) {
       // =============================================================== MMA issue
       // Operand descriptors of stage 0; a stage, a block and a K-step are plain address offsets.
@@ -465,9 +501,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     const int part = a.rev ? 0 : n - 1;  // the one chunk that the sequence's end may cut
     const int nv_part = n > 0 ? valid(part) : LQ;
     const uint32_t sPow = sBase + C::OFF_POW;
-    auto weigh = [&](int i) -> bool {
+    auto weigh = [&](int i) {
       const int s = i & 1, nv = i == part ? nv_part : LQ;
-      if (!la_wait(B(LB_LV + s), (uint32_t)((i >> 1) & 1), abort_flag)) return false;
       const bool in = t < nv;
       const float wt = in ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
       const uint64_t w2 = f2(wt, wt), minus = f2(-1.0f, -1.0f);
@@ -494,7 +529,6 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         }
       }
       if (nv < LQ) {  // no infinity or NaN found past the length meets a product
-        if (!la_wait(B(LB_LQK + s), (uint32_t)((i >> 1) & 1), abort_flag)) return false;
         if (t >= nv) {
           const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -507,7 +541,6 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       }
       fence_async_smem();
       arrive(LB_VT);
-      return true;
     };
 
     // the decay of a full chunk as two floats: a long memory multiplies it in hundreds of times
@@ -518,19 +551,17 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     const uint32_t keep = a.rev ? kFull << lane : kFull >> (31 - lane);
     const float rowf = d > 0 ? a.s_upd * a.s_out * lds32(sPow + 4 * (a.rev ? 32 * d - lane : 32 * d - 31 + lane)) : 0.0f;
     auto out_row = [&](int64_t tok) { return (((int64_t)bi * a.L + tok) * a.H + h) * (int64_t)a.VD + col; };
-    bool ok = true;
     if (n > 0) {
       if constexpr (FULL) publish();
-      ok = weigh(0);
+      named_bar_sync(LN_H, LN_THREADS);
+      weigh(0);
     }
-    for (int i = 0; ok && i < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       const int s = i & 1;
-      const uint32_t p = (uint32_t)(i & 1);
       const int nv = i == part ? nv_part : LQ;
       if constexpr (FULL) {
         // ---- scores: rows of this quarter, 32 columns
-        ok = la_wait(B(LB_SC), p, abort_flag);
-        if (!ok) break;
+        named_bar_sync(LN_SC, LN_THREADS);
         tc_fence_after();
         uint32_t o[16];
         if (d < 0) {
@@ -574,8 +605,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         arrive(LB_SP);
       }
       // ---- the next chunk's weighted v, once the update has read this one's; the state
-      ok = la_wait(B(LB_H), p, abort_flag);
-      if (!ok) break;
+      named_bar_sync(LN_H, LN_THREADS);
       tc_fence_after();
       const float ghi = nv == LQ ? a128 : lds32(sPow + 4 * nv), glo = nv == LQ ? a128_lo : 0.0f;
 #pragma unroll
@@ -594,16 +624,14 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       }
       tc_fence_before();
       arrive(LB_HC);
-      if (i + 1 < n && !weigh(i + 1)) break;
+      if (i + 1 < n) weigh(i + 1);
       if constexpr (FULL) {
         if (i + 1 < n) {
-          ok = la_wait(B(LB_YI), p, abort_flag);  // Yi has read the copy before
-          if (!ok) break;
+          named_bar_sync(LN_YI, LN_THREADS);  // Yi has read the copy before
           publish();
         }
         // ---- outputs of the chunk
-        ok = la_wait(B(LB_Y), p, abort_flag);
-        if (!ok) break;
+        named_bar_sync(LN_Y, LN_THREADS);
         tc_fence_after();
         const bool on = t < nv;
         const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
@@ -641,7 +669,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     }
 #pragma unroll
     for (int e = 0; e < LSC / 2; ++e) f2_split(S2[e], S[2 * e], S[2 * e + 1]);
-    if (ok && !*abort_flag && owner && page >= 0) {
+    if (!*abort_flag && owner && page >= 0) {
       if (!FULL) {
         store_slot(seg + 1);
       } else if (seg == a.nseg - 1 && a.s_fin) {
