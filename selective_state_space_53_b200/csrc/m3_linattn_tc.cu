@@ -23,16 +23,17 @@
 // Warp roles (20 warps; every mbarrier wait is bounded by %globaltimer):
 //   0      producer: TMA loads of q, k, v into two stages (128-byte swizzle)
 //   1      MMA issue; tensor-memory allocation
-//   2      output store: TMA from the tile that the outputs were staged in (over the chunk's q)
-//   3      signals: waits for products and copies on behalf of
-//   4-19   everything else, all sixteen warps on one task at a time, four warps (one per quarter of the
-//          rows) to 16 value columns (scores: to 32 score columns), so that a task's latency is a quarter and four warps of the
-//          same code hide each other's latencies on every scheduler.  Per chunk i: the scores A -> A'; the
-//          state after i, once the update is complete, and the weighted v of i + 1, whose buffer it has then
-//          read; bf16(S) to shared memory; the outputs of i
-// MMA order per chunk i: update(i), Yi(i), Ya(i), A(i+1), so that each SIMT task runs behind products
-// that do not need it: the scores behind update and Yi, the weighted v and the state behind Yi to A(i+1),
-// the outputs behind A(i+1) and the next update.
+//   2      signals for the score warps; output store: TMA from the tile that the outputs were staged in
+//          (over the chunk's q)
+//   3      signals for the state warps
+//   4-11   scores A -> A', 64 columns a warp, and the outputs of 32 value columns
+//   12-19  the state of 32 value columns in registers, its copy bf16(S), and the weighted v
+// Each kind has two warps on every scheduler, so that the tasks of one fill the latencies of the other.
+// The signal warps wait for the products and the copies and meet the others on named barriers, where a
+// waiting warp takes no issue slots (polling took a third of them).
+// MMA order per chunk i: update(i), Yi(i), Ya(i), A(i+1).  The scores of i run behind update and Yi, the
+// outputs behind A(i+1) and the next update; the weighted v of i + 1 (whose buffer the update of i has
+// read then) and the state behind Yi to A(i+1).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,13 +45,14 @@ namespace {
 
 constexpr int LQ = 128;  // tokens of a chunk
 constexpr int LV = 64;   // value columns of a CTA
-constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2, L_SIGNAL = 3;
+constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2, L_SIGNAL = 3;  // L_STORE also signals the score group
 constexpr int L_CTRL = 4;       // control warps
 constexpr int L_THREADS = 640;
-constexpr int L_SIMT = 16;     // warps of the SIMT tasks
-// named barriers of the SIMT warps and the signal warp: what the SIMT warps wait for
-constexpr uint32_t LN_SC = 1, LN_H = 2, LN_YI = 3, LN_Y = 4, LN_THREADS = 32 * (L_SIMT + 1);
-constexpr int LSC = LV / 4;    // value columns of a warpgroup
+constexpr int L_PREFETCH = 4;  // chunks that L2 is asked for ahead of their loads
+constexpr int L_GROUP = 8;     // warps of the score group and of the state group
+constexpr int LSC = LV / 2;    // value columns of a warp of either group
+// named barriers of a signal warp and its group: what the group waits for
+constexpr uint32_t LN_SC = 1, LN_Y = 2, LN_H = 3, LN_YI = 4, LN_THREADS = 32 * (L_GROUP + 1);
 constexpr unsigned long long L_WAIT_NS = 2000000000ull;  // 2 s bound on any wait
 constexpr int LBLK = 128 * 128;                          // one 64-column block of a 128-row tile, bytes
 constexpr int L_MAXPOW = LQ + 1;
@@ -165,6 +167,13 @@ __device__ __forceinline__ void mma_commit1(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// Asks L2 for a tile that a load will want later.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 // TMA tile store from shared memory, in bulk groups.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
@@ -238,10 +247,10 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       for (int k : {LB_LQK, LB_LV, LB_FK, LB_FQ, LB_FV}) mbar_init(&bar[k + s], 1);
-      mbar_init(&bar[LB_YW + s], L_SIMT);
+      mbar_init(&bar[LB_YW + s], L_GROUP);
     }
     for (int k : {LB_SC, LB_H, LB_YI, LB_Y}) mbar_init(&bar[k], 1);
-    for (int k : {LB_SP, LB_ST, LB_HC, LB_VT, LB_YE}) mbar_init(&bar[k], L_SIMT);
+    for (int k : {LB_SP, LB_ST, LB_HC, LB_VT, LB_YE}) mbar_init(&bar[k], L_GROUP);
     mbar_init(&bar[LB_DRAIN], 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -272,13 +281,36 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     return left < LQ ? (int)left : LQ;
   };
 
+  const int part = a.rev ? 0 : n - 1;  // the one chunk that the sequence's end may cut
+  const int nv_part = n > 0 ? valid(part) : LQ;
+  const uint32_t sPow = sBase + C::OFF_POW;
+  auto arrive = [&](int k) {
+    __syncwarp();
+    if (lane == 0) la_arrive(B(k));
+  };
+
   if (warp < L_CTRL) {
     if (warp == L_PROD) {
       // =============================================================== producer
       if (lane == 0) {
         const int gq = h / (a.H / a.hq), gk = h / (a.H / a.hk), gv = h / (a.H / a.hv);
+        // chunk i into L2 (q and k by the CTA of the first value columns only): two stages in shared memory
+        // alone leave a load's latency, three thousand cycles from HBM, uncovered
+        auto prefetch = [&](int i) {
+          if (i >= n) return;
+          const int tok = (int)(chunk(i) * LQ);
+          tma_prefetch_4d(&tmV, LV * vt, gv, tok, bi);
+          if (vt > 0) return;
+#pragma unroll
+          for (int b = 0; b < KD / 64; ++b) {
+            tma_prefetch_4d(&tmK, 64 * b, gk, tok, bi);
+            if constexpr (FULL) tma_prefetch_4d(&tmQ, 64 * b, gq, tok, bi);
+          }
+        };
+        for (int i = 2; i < L_PREFETCH; ++i) prefetch(i);
         int done = 0;
         for (int i = 0; i < n; ++i) {
+          prefetch(i + L_PREFETCH);
           const int s = i & 1, tok = (int)(chunk(i) * LQ);
           const uint32_t before = (uint32_t)(((i >> 1) & 1) ^ 1);  // phase of the stage's chunk i - 2
           if (i >= 2 && !la_wait(B(LB_FK + s), before, abort_flag)) break;
@@ -303,53 +335,52 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         }
       }
     } else if (warp == L_STORE) {
-      // =============================================================== output store
+      // =============================================================== signals to the score group, output store
+      // After a timeout a signal warp meets its group without waiting, so that the group runs through its
+      // chunks (within bounds, the results void) and everyone leaves.
       if constexpr (FULL) {
-        if (lane == 0) {
-          for (int i = 0; i < n; ++i) {
-            const int s = i & 1;
-            if (!la_wait(B(LB_YW + s), (uint32_t)((i >> 1) & 1), abort_flag)) break;
-            if (!a.out_f32) {  // tokens past L are not written
+        bool ok = true;
+        auto store = [&](int i) {  // the staged outputs of chunk i; tokens past L are not written
+          const int s = i & 1;
+          ok = ok && la_wait(B(LB_YW + s), (uint32_t)((i >> 1) & 1), abort_flag);
+          if (lane == 0 && ok) {
+            if (!a.out_f32) {
               tma_store_4d(&tmO, sQ(s), LV * vt, h, (int)(chunk(i) * LQ), bi);
               bulk_commit();
               bulk_wait_read();
             }
             la_arrive(B(LB_FQ + s));
           }
-          bulk_wait_all();
-        }
-      }
-    } else if (warp == L_SIGNAL) {
-      // =============================================================== signals
-      // Waits for the products and the v copies on behalf of the SIMT warps and meets them on a named barrier,
-      // where a waiting warp takes no issue slots.  After a timeout it meets them without waiting, so that
-      // they run through their chunks (within bounds, the results void) and everyone leaves.
-      bool ok = true;
-      if (n > 0) {
-        ok = la_wait(B(LB_LV), 0, abort_flag) && la_wait(B(LB_LQK), 0, abort_flag);
-        named_bar_sync(LN_H, LN_THREADS);
-      }
-      for (int i = 0; i < n; ++i) {
-        const uint32_t p = (uint32_t)(i & 1);
-        if constexpr (FULL) {
+          __syncwarp();
+        };
+        for (int i = 0; i < n; ++i) {
+          const uint32_t p = (uint32_t)(i & 1);
           ok = ok && la_wait(B(LB_SC), p, abort_flag);
           named_bar_sync(LN_SC, LN_THREADS);
+          if (i > 0) store(i - 1);
+          ok = ok && la_wait(B(LB_Y), p, abort_flag);
+          named_bar_sync(LN_Y, LN_THREADS);
         }
-        ok = ok && la_wait(B(LB_H), p, abort_flag);
-        if (i + 1 < n) {  // the next chunk's v, and k where the sequence's end cuts the chunk
+        if (n > 0) store(n - 1);
+        if (lane == 0) bulk_wait_all();
+      }
+    } else if (warp == L_SIGNAL) {
+      // =============================================================== signals to the state group
+      bool ok = true;
+      for (int i = -1; n > 0 && i < n; ++i) {  // the update of i complete (i = -1: none yet), v of i + 1 landed
+        const uint32_t p = (uint32_t)(i & 1);
+        if (i >= 0) ok = ok && la_wait(B(LB_H), p, abort_flag);
+        if (i + 1 < n) {
           const int s = (i + 1) & 1;
           const uint32_t ps = (uint32_t)(((i + 1) >> 1) & 1);
           ok = ok && la_wait(B(LB_LV + s), ps, abort_flag);
-          if (valid(i + 1) < LQ) ok = ok && la_wait(B(LB_LQK + s), ps, abort_flag);
+          // k as well where the sequence's end cuts the chunk
+          if (i + 1 == part && nv_part < LQ) ok = ok && la_wait(B(LB_LQK + s), ps, abort_flag);
         }
         named_bar_sync(LN_H, LN_THREADS);
-        if constexpr (FULL) {
-          if (i + 1 < n) {
-            ok = ok && la_wait(B(LB_YI), p, abort_flag);
-            named_bar_sync(LN_YI, LN_THREADS);
-          }
-          ok = ok && la_wait(B(LB_Y), p, abort_flag);
-          named_bar_sync(LN_Y, LN_THREADS);
+        if (FULL && i >= 0 && i + 1 < n) {
+          ok = ok && la_wait(B(LB_YI), p, abort_flag);
+          named_bar_sync(LN_YI, LN_THREADS);
         }
       }
     } else if (warp == L_MMA && n > 0) {
@@ -425,30 +456,145 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       __syncwarp();
       la_drain(B(LB_DRAIN), 0);
     }
+  } else if (warp < L_CTRL + L_GROUP) {
+    // =============================================================== scores and outputs
+    if constexpr (FULL) {
+      const int w = (warp - L_CTRL) >> 2;  // score blocks w and 3 - w (of 32 columns), value columns 32 w ..
+      const int t = 32 * q4 + lane;        // this thread's token of a chunk
+      const uint32_t ro = (uint32_t)t * 128u;
+      const int64_t col = LV * vt + LSC * w;
+      // diagonal blocks: the weight of column e lies e words on (mirrored table), kept where bit e is set
+      const uint32_t sDg = sBase + C::OFF_DIAG + 4 * (31 - lane), sCol = sBase + C::OFF_COL;
+      const uint32_t keep = a.rev ? kFull << lane : kFull >> (31 - lane);
+      const float sc = a.s_upd * a.s_out;
+      auto out_row = [&](int64_t tok) { return (((int64_t)bi * a.L + tok) * a.H + h) * (int64_t)a.VD + col; };
+      for (int i = 0; i < n; ++i) {
+        const int s = i & 1;
+        const int nv = i == part ? nv_part : LQ;
+        named_bar_sync(LN_SC, LN_THREADS);
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int cb = half ? 3 - w : w;           // block of columns
+          const int d = a.rev ? cb - q4 : q4 - cb;  // blocks between the rows and the columns
+          uint32_t o[16];
+          if (d < 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          } else {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb, v);
+            if (d > 0) {
+              const float r = sc * lds32(sPow + 4 * (a.rev ? 32 * d - lane : 32 * d - 31 + lane));
+              const uint64_t r2 = f2(r, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint4 u = lds128(sCol + 16 * e);
+                float x0, x1, x2, x3;
+                f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
+                f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
+                o[2 * e] = pack_bf16(x0, x1);
+                o[2 * e + 1] = pack_bf16(x2, x3);
+              }
+            } else {
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                // a select: what lies ahead may be infinite
+                const float x0 = __uint_as_float(v[2 * e]) * lds32(sDg + 8 * e);
+                const float x1 = __uint_as_float(v[2 * e + 1]) * lds32(sDg + 8 * e + 4);
+                o[e] = pack_bf16((keep >> (2 * e)) & 1 ? x0 : 0.0f, (keep >> (2 * e + 1)) & 1 ? x1 : 0.0f);
+              }
+            }
+            if (32 * cb + 32 > nv) {  // columns past the length
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (32 * cb + 2 * e >= nv) o[e] = 0u;
+                else if (32 * cb + 2 * e + 1 >= nv) o[e] &= 0xffffu;
+              }
+            }
+          }
+          tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(LB_SP);
+        // ---- outputs of the chunk
+        named_bar_sync(LN_Y, LN_THREADS);
+        tc_fence_after();
+        const bool on = t < nv;
+        const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
+        const int64_t tok = chunk(i) * LQ + t;
+#pragma unroll
+        for (int c = 0; c < LSC / 16; ++c) {
+          uint32_t x[16], y[16];
+          tmem_ld16(tmem + lane_base + C::TM_YI + LSC * w + 16 * c, x);
+          tmem_ld16(tmem + lane_base + C::TM_YA + LSC * w + 16 * c, y);
+          tmem_wait_ld();
+          if (c == LSC / 16 - 1) {
+            tc_fence_before();
+            arrive(LB_YE);
+          }
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            f2_split(f2_fma(f2(f, f), f2_bits(x[2 * e], x[2 * e + 1]), f2_bits(y[2 * e], y[2 * e + 1])), v[2 * e], v[2 * e + 1]);
+          if (!on) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+          }
+          if (a.out_f32) {
+            if (tok < a.L) {
+              float4* g = reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row(tok)) + 4 * c;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) g[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+          } else {  // over q of the stage, which Yi was the last to read
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              sts128(sQ(s) + ro + (((4 * w + 2 * c + e) ^ (t & 7)) << 4),
+                     make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                                pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7])));
+          }
+        }
+        fence_async_smem();
+        arrive(LB_YW + s);
+      }
+      // chunks past the sequence's length
+      for (int64_t j = cs.z0; j < cs.z1; ++j) {
+        const int64_t tok = j * LQ + t;
+        if (tok >= a.L) continue;
+        const int e = a.out_f32 ? 4 : 2;
+        uint4* g = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + out_row(tok) * e);
+        for (int c = 0; c < LSC * e / 16; ++c) g[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
   } else {
-    // =============================================================== scores, weighted v, state, outputs
-    const int w = (warp - L_CTRL) >> 2;            // value columns 16 w .. 16 w + 15, score columns 32 w .. 32 w + 31
-    const int t = 32 * q4 + lane;    // this thread's token of a chunk (scores, weighted v, outputs)
+    // =============================================================== state and weighted v
+    const int w = (warp - L_CTRL - L_GROUP) >> 2;  // value columns 32 w .. 32 w + 31
+    const int t = 32 * q4 + lane;                  // this thread's token of a chunk (weighted v)
     const uint32_t ro = (uint32_t)t * 128u;
     // accumulator row of the state (M = 128: the lane; M = 64: lanes 0-15 of each quarter)
     const bool owner = KD == 128 || lane < 16;
     const int row = KD == 128 ? t : 16 * q4 + (lane & 15);
     const int64_t col = LV * vt + LSC * w;
-    auto arrive = [&](int k) {
-      __syncwarp();
-      if (lane == 0) la_arrive(B(k));
-    };
 
-    // ---- the state entering the segment
-    float S[LSC];
+    // ---- the state entering the segment, in pairs
+    uint64_t S[LSC / 2];
 #pragma unroll
-    for (int e = 0; e < LSC; ++e) S[e] = 0.0f;
+    for (int e = 0; e < LSC / 2; ++e) S[e] = 0;
     auto slot = [&](int s) { return a.ws + ((bh * a.nseg + s) * KD + row) * (int64_t)a.VD + col; };
     const int64_t sbase = (page * a.H + h) * (int64_t)KD * a.VD + row * a.s_i + col * a.s_j;
     auto store_slot = [&](int s) {
       float4* p = reinterpret_cast<float4*>(slot(s));
 #pragma unroll
-      for (int e = 0; e < LSC / 4; ++e) p[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+      for (int e = 0; e < LSC / 4; ++e) {
+        float4 v;
+        f2_split(S[2 * e], v.x, v.y);
+        f2_split(S[2 * e + 1], v.z, v.w);
+        p[e] = v;
+      }
     };
     if (owner && page >= 0) {
       if (seg == 0) {
@@ -457,7 +603,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
           const float* src = from_ws ? slot(0) : a.s_in + sbase;
           const int64_t sj = from_ws ? 1 : a.s_j;
 #pragma unroll
-          for (int e = 0; e < LSC; ++e) S[e] = src[e * sj];
+          for (int e = 0; e < LSC / 2; ++e) S[e] = f2(src[2 * e * sj], src[(2 * e + 1) * sj]);
         }
         if (!FULL) store_slot(0);
       } else if (FULL) {
@@ -467,146 +613,92 @@ __global__ void __launch_bounds__(L_THREADS, 1)
 #pragma unroll
           for (int e = 0; e < LSC / 4; ++e) {
             const float4 v = z[e];
-            S[4 * e] = fmaf(f, S[4 * e], v.x);
-            S[4 * e + 1] = fmaf(f, S[4 * e + 1], v.y);
-            S[4 * e + 2] = fmaf(f, S[4 * e + 2], v.z);
-            S[4 * e + 3] = fmaf(f, S[4 * e + 3], v.w);
+            S[2 * e] = f2_fma(f2(f, f), S[2 * e], f2(v.x, v.y));
+            S[2 * e + 1] = f2_fma(f2(f, f), S[2 * e + 1], f2(v.z, v.w));
           }
         }
       }
     }
-    uint64_t S2[LSC / 2];  // the state from here on, in pairs
-#pragma unroll
-    for (int e = 0; e < LSC / 2; ++e) S2[e] = f2(S[2 * e], S[2 * e + 1]);
     auto publish = [&]() {  // bf16(S), the B operand of Yi
       if (owner) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < LSC / 8; ++c) {
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float lo, hi;
-            f2_split(S2[4 * c + e], lo, hi);
+            f2_split(S[4 * c + e], lo, hi);
             o[e] = pack_bf16(lo, hi);
           }
-          sts128(sS + row * 128 + (((c + 2 * w) ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(sS + row * 128 + (((c + 4 * w) ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
       fence_async_smem();
       arrive(LB_ST);
     };
 
-    // ---- the weighted v of chunk i: three parts of this thread's 16 values; each part takes the upper 16
-    // bits of what is left, 24 bits in all
-    const int part = a.rev ? 0 : n - 1;  // the one chunk that the sequence's end may cut
-    const int nv_part = n > 0 ? valid(part) : LQ;
-    const uint32_t sPow = sBase + C::OFF_POW;
-    auto weigh = [&](int i) {
-      const int s = i & 1, nv = i == part ? nv_part : LQ;
-      const bool in = t < nv;
-      const float wt = in ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
-      const uint64_t w2 = f2(wt, wt), minus = f2(-1.0f, -1.0f);
+    // ---- the weighted v of chunk i: three parts of 8 values; each part takes the upper 16 bits of what
+    // is left, 24 bits in all
+    auto weight = [&](int i) {
+      const int nv = i == part ? nv_part : LQ;
+      return t < nv ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
+    };
+    auto vchunk = [&](int c) { return ro + (uint32_t)(((c + 4 * w) ^ (t & 7)) << 4); };
+    auto finish = [&](int i) {  // the weighted v is complete
+      if (i == part && t >= nv_part) {  // no infinity or NaN found past the length meets a product
+        const int s = i & 1;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t off = ro + (uint32_t)(((c + 2 * w) ^ (t & 7)) << 4);
-        uint4 raw = lds128(sV(s) + off);
-        if (!in) raw = make_uint4(0, 0, 0, 0);  // past the length there may be anything
-        uint64_t f[4] = {f2_mul(f2(bf_lo(raw.x), bf_hi(raw.x)), w2), f2_mul(f2(bf_lo(raw.y), bf_hi(raw.y)), w2),
-                         f2_mul(f2(bf_lo(raw.z), bf_hi(raw.z)), w2), f2_mul(f2(bf_lo(raw.w), bf_hi(raw.w)), w2)};
+        for (int c = 4 * w; c < 4 * w + 4; ++c) {
+          sts128(sV(s) + ro + 16 * c, zero);
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            f2_split(f[e], lo, hi);
-            o[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-            if (q < 2)  // exact
-              f[e] = f2_fma(f2(__uint_as_float(__float_as_uint(lo) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(hi) & 0xffff0000u)), minus, f[e]);
-          }
-          sts128(sVT + q * LBLK + off, make_uint4(o[0], o[1], o[2], o[3]));
-        }
-      }
-      if (nv < LQ) {  // no infinity or NaN found past the length meets a product
-        if (t >= nv) {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int c = 2 * w; c < 2 * w + 2; ++c) {
-            sts128(sV(s) + ro + 16 * c, zero);
-#pragma unroll
-            for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + ro + 16 * c, zero);
-          }
+          for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + ro + 16 * c, zero);
         }
       }
       fence_async_smem();
       arrive(LB_VT);
     };
+    auto weigh = [&](int i) {
+      const float wt = weight(i);
+      const uint64_t w2 = f2(wt, wt), minus = f2(-1.0f, -1.0f);
+#pragma unroll
+      for (int c = 0; c < LSC / 8; ++c) {
+        uint4 raw = lds128(sV(i & 1) + vchunk(c));
+        if (i == part && t >= nv_part) raw = make_uint4(0, 0, 0, 0);  // past the length there may be anything
+        uint64_t f[4] = {f2_mul(f2(bf_lo(raw.x), bf_hi(raw.x)), w2), f2_mul(f2(bf_lo(raw.y), bf_hi(raw.y)), w2),
+                         f2_mul(f2(bf_lo(raw.z), bf_hi(raw.z)), w2), f2_mul(f2(bf_lo(raw.w), bf_hi(raw.w)), w2)};
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            f2_split(f[e], lo, hi);
+            b[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            if (q < 2)  // exact
+              f[e] = f2_fma(f2(__uint_as_float(__float_as_uint(lo) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(hi) & 0xffff0000u)), minus, f[e]);
+          }
+          sts128(sVT + q * LBLK + vchunk(c), make_uint4(b[0], b[1], b[2], b[3]));
+        }
+      }
+      finish(i);
+    };
 
     // the decay of a full chunk as two floats: a long memory multiplies it in hundreds of times
     const float a128 = lds32(sPow + 4 * LQ), a128_lo = (float)(la_pow(ld, LQ) - (double)a128);
-    const int d = a.rev ? w - q4 : q4 - w;  // score blocks between this warp's rows and columns
-    // diagonal blocks: the weight of column e lies e words on (mirrored table), kept where bit e is set
-    const uint32_t sDg = sBase + C::OFF_DIAG + 4 * (31 - lane), sCol = sBase + C::OFF_COL;
-    const uint32_t keep = a.rev ? kFull << lane : kFull >> (31 - lane);
-    const float rowf = d > 0 ? a.s_upd * a.s_out * lds32(sPow + 4 * (a.rev ? 32 * d - lane : 32 * d - 31 + lane)) : 0.0f;
-    auto out_row = [&](int64_t tok) { return (((int64_t)bi * a.L + tok) * a.H + h) * (int64_t)a.VD + col; };
     if (n > 0) {
       if constexpr (FULL) publish();
       named_bar_sync(LN_H, LN_THREADS);
       weigh(0);
     }
     for (int i = 0; i < n; ++i) {
-      const int s = i & 1;
       const int nv = i == part ? nv_part : LQ;
-      if constexpr (FULL) {
-        // ---- scores: rows of this quarter, 32 columns
-        named_bar_sync(LN_SC, LN_THREADS);
-        tc_fence_after();
-        uint32_t o[16];
-        if (d < 0) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0u;
-        } else {
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_base + C::TM_A + 32 * w, v);
-          tmem_wait_ld();
-          if (d > 0) {
-            const uint64_t r2 = f2(rowf, rowf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 u = lds128(sCol + 16 * e);
-              float x0, x1, x2, x3;
-              f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
-              f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
-              o[2 * e] = pack_bf16(x0, x1);
-              o[2 * e + 1] = pack_bf16(x2, x3);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              // a select: what lies ahead may be infinite
-              const float x0 = __uint_as_float(v[2 * e]) * lds32(sDg + 8 * e);
-              const float x1 = __uint_as_float(v[2 * e + 1]) * lds32(sDg + 8 * e + 4);
-              o[e] = pack_bf16((keep >> (2 * e)) & 1 ? x0 : 0.0f, (keep >> (2 * e + 1)) & 1 ? x1 : 0.0f);
-            }
-          }
-          if (32 * w + 32 > nv) {  // columns past the length
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (32 * w + 2 * e >= nv) o[e] = 0u;
-              else if (32 * w + 2 * e + 1 >= nv) o[e] &= 0xffffu;
-            }
-          }
-        }
-        tmem_st16(tmem + lane_base + C::TM_AP + 16 * w, o);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(LB_SP);
-      }
-      // ---- the next chunk's weighted v, once the update has read this one's; the state
+      // ---- the next chunk's weighted v, once the update has read this one's
       named_bar_sync(LN_H, LN_THREADS);
       tc_fence_after();
+      if (i + 1 < n) weigh(i + 1);
+      // ---- the state after this chunk
       const float ghi = nv == LQ ? a128 : lds32(sPow + 4 * nv), glo = nv == LQ ? a128_lo : 0.0f;
 #pragma unroll
       for (int c = 0; c < LSC / 8; ++c) {
@@ -619,71 +711,27 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         for (int e = 0; e < 4; ++e) {
           const uint64_t hs = f2_add(f2_bits(x[2 * e], x[2 * e + 1]),
                                      f2_add(f2_bits(y[2 * e], y[2 * e + 1]), f2_bits(z[2 * e], z[2 * e + 1])));
-          S2[4 * c + e] = f2_fma(f2(ghi, ghi), S2[4 * c + e], f2_fma(f2(glo, glo), S2[4 * c + e], hs));
+          S[4 * c + e] = f2_fma(f2(ghi, ghi), S[4 * c + e], f2_fma(f2(glo, glo), S[4 * c + e], hs));
         }
       }
       tc_fence_before();
       arrive(LB_HC);
-      if (i + 1 < n) weigh(i + 1);
-      if constexpr (FULL) {
-        if (i + 1 < n) {
-          named_bar_sync(LN_YI, LN_THREADS);  // Yi has read the copy before
-          publish();
-        }
-        // ---- outputs of the chunk
-        named_bar_sync(LN_Y, LN_THREADS);
-        tc_fence_after();
-        const bool on = t < nv;
-        const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
-        uint32_t x[16], y[16];
-        tmem_ld16(tmem + lane_base + C::TM_YI + LSC * w, x);
-        tmem_ld16(tmem + lane_base + C::TM_YA + LSC * w, y);
-        tmem_wait_ld();
-        tc_fence_before();
-        arrive(LB_YE);
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          f2_split(f2_fma(f2(f, f), f2_bits(x[2 * e], x[2 * e + 1]), f2_bits(y[2 * e], y[2 * e + 1])), v[2 * e], v[2 * e + 1]);
-        if (!on) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-        }
-        if (a.out_f32) {
-          const int64_t tok = chunk(i) * LQ + t;
-          if (tok < a.L) {
-            float4* g = reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row(tok));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          }
-        } else {  // over q of the stage, which Yi was the last to read
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            sts128(sQ(s) + ro + (((c + 2 * w) ^ (t & 7)) << 4),
-                   make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                              pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7])));
-          fence_async_smem();
-        }
-        arrive(LB_YW + s);
+      if (FULL && i + 1 < n) {
+        named_bar_sync(LN_YI, LN_THREADS);  // Yi has read the copy before
+        publish();
       }
     }
-#pragma unroll
-    for (int e = 0; e < LSC / 2; ++e) f2_split(S2[e], S[2 * e], S[2 * e + 1]);
     if (!*abort_flag && owner && page >= 0) {
       if (!FULL) {
         store_slot(seg + 1);
       } else if (seg == a.nseg - 1 && a.s_fin) {
 #pragma unroll
-        for (int e = 0; e < LSC; ++e) a.s_fin[sbase + e * a.s_j] = S[e];
-      }
-    }
-    if constexpr (FULL) {  // chunks past the sequence's length
-      for (int64_t j = cs.z0; j < cs.z1; ++j) {
-        const int64_t tok = j * LQ + t;
-        if (tok >= a.L) continue;
-        const int e = a.out_f32 ? 4 : 2;
-        uint4* g = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + out_row(tok) * e);
-        for (int c = 0; c < LSC * e / 16; ++c) g[c] = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < LSC / 2; ++e) {
+          float lo, hi;
+          f2_split(S[e], lo, hi);
+          a.s_fin[sbase + 2 * e * a.s_j] = lo;
+          a.s_fin[sbase + (2 * e + 1) * a.s_j] = hi;
+        }
       }
     }
   }
