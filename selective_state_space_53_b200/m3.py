@@ -297,16 +297,19 @@ def scan_backward(dims: Dims, dev: dict, state0: State, dy, dh_final=None, strea
     return out
 
 
-def _on_stream(device, stream):
-    """Context in which a call on tensors of `device` runs: that device current and `stream` (or the
-    device's current stream) the one that allocations and launches go to."""
-    import contextlib
+def _call_stream(index, stream):
+    """Raw handle of the stream a call on tensors of CUDA device `index` runs on: `stream`, or the device's
+    current one.  None when the call has to switch to that device or stream first (``_elsewhere``)."""
     import torch
-    if stream is not None:
-        return torch.cuda.stream(stream)  # also makes the stream's device current
-    if device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
+
+
+def _elsewhere(device, stream):
+    """Context that makes the device current, and `stream` if given (allocations then belong to it too)."""
+    import torch
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
 def _expect(what, name, t, shape, dtype, device):
@@ -323,22 +326,26 @@ def _expect(what, name, t, shape, dtype, device):
 def _la_dims(what, q, k, v, log_decay, token):
     """Dims of a linear attention call from its tensors, after their checks (token: no L axis)."""
     import torch
-    if q.dim() != (3 if token else 4) or v.dim() != q.dim():
-        raise M3Error(-1, f"{what}: q has {q.dim()} and v {v.dim()} dimensions, expected {3 if token else 4}")
-    if q.dtype == torch.bfloat16:
+    sq, sv, dtype, dev = q.shape, v.shape, q.dtype, q.device
+    if len(sq) != (3 if token else 4) or len(sv) != len(sq):
+        raise M3Error(-1, f"{what}: q has {len(sq)} and v {len(sv)} dimensions, expected {3 if token else 4}")
+    if dtype is torch.bfloat16:
         dt = M3_BF16
-    elif q.dtype == torch.float32:
+    elif dtype is torch.float32:
         dt = M3_F32
     else:
-        raise M3Error(-2, f"{what}: q is {q.dtype}, expected bfloat16 or float32")
-    b, G, N = q.shape[0], q.shape[-2], q.shape[-1]
-    H, P = v.shape[-2:]
-    L = 1 if token else q.shape[1]
-    dev = q.device
-    _expect(what, "q", q, q.shape, q.dtype, dev)
-    _expect(what, "k", k, q.shape, q.dtype, dev)
-    _expect(what, "v", v, (b, H, P) if token else (b, L, H, P), q.dtype, dev)
-    _expect(what, "log_decay", log_decay, (H,), torch.float32, dev)
+        raise M3Error(-2, f"{what}: q is {dtype}, expected bfloat16 or float32")
+    b, G, N = sq[0], sq[-2], sq[-1]
+    H, P = sv[-2], sv[-1]
+    L = 1 if token else sq[1]
+    if not (sv[0] == b and (token or sv[1] == L) and k.shape == sq and k.dtype is dtype and v.dtype is dtype
+            and log_decay.dtype is torch.float32 and log_decay.shape == (H,) and dev.type == "cuda"
+            and k.device == dev and v.device == dev and log_decay.device == dev and q.is_contiguous()
+            and k.is_contiguous() and v.is_contiguous() and log_decay.is_contiguous()):
+        _expect(what, "q", q, sq, dtype, dev)
+        _expect(what, "k", k, sq, dtype, dev)
+        _expect(what, "v", v, (b, H, P) if token else (b, L, H, P), dtype, dev)
+        _expect(what, "log_decay", log_decay, (H,), torch.float32, dev)
     return Dims(b, L, H, P, N, 1, G, 0, dt, 0)
 
 
@@ -350,6 +357,10 @@ def _la_rows(what, dims, state, pages, device):
     if pages is not None:
         _expect(what, "pages", pages, (dims.b,), torch.int32, device)
     return rows
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def m3_linattn_workspace_size(dims: Dims) -> int:
@@ -403,16 +414,22 @@ def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y
     rows = dims.b if state is None else _la_rows(what, dims, state, pages, dev)
     if y is not None:
         _expect(what, "y", y, v.shape, v.dtype, dev)
-    with _on_stream(dev, stream):
-        out = state if state is not None else torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32,
-                                                          device=dev)
-        if y is None:
-            y = torch.empty_like(v)
-        if workspace is None:
-            n = m3_linattn_workspace_size(dims)
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        m3_linattn_fwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state, out, rows,
-                       pages, y, workspace)
+    raw = _call_stream(dev.index, stream)
+    if raw is None:
+        with _elsewhere(dev, stream):
+            return linattn(q, k, v, log_decay, scale, lens, state, pages, y, workspace)
+    out = state
+    if out is None:
+        out = torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)
+    if y is None:
+        y = torch.empty_like(v)
+    if workspace is None:
+        n = m3_linattn_workspace_size(dims)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().m3_linattn_fwd(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                dims.N ** -0.5 if scale is None else scale, _adr(lens), _adr(state), out.data_ptr(),
+                                rows, _adr(pages), y.data_ptr(), _adr(workspace), ws_bytes, raw), "m3_linattn_fwd")
     return y, out
 
 
@@ -422,13 +439,19 @@ def linattn_step(q, k, v, log_decay, state, scale=None, pages=None, y=None, stre
     import torch
     what = "linattn_step"
     dims = _la_dims(what, q, k, v, log_decay, True)
-    rows = _la_rows(what, dims, state, pages, q.device)
+    dev = q.device
+    rows = _la_rows(what, dims, state, pages, dev)
     if y is not None:
-        _expect(what, "y", y, v.shape, v.dtype, q.device)
-    with _on_stream(q.device, stream):
-        if y is None:
-            y = torch.empty_like(v)
-        m3_linattn_step(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, state, rows, pages, y)
+        _expect(what, "y", y, v.shape, v.dtype, dev)
+    raw = _call_stream(dev.index, stream)
+    if raw is None:
+        with _elsewhere(dev, stream):
+            return linattn_step(q, k, v, log_decay, state, scale, pages, y)
+    if y is None:
+        y = torch.empty_like(v)
+    _check(lib().m3_linattn_step(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                 dims.N ** -0.5 if scale is None else scale, state.data_ptr(), rows, _adr(pages),
+                                 y.data_ptr(), raw), "m3_linattn_step")
     return y
 
 
@@ -446,13 +469,18 @@ def linattn_backward(q, k, v, log_decay, dy, scale=None, lens=None, state0=None,
     for name, t in (("state0", state0), ("dstate", dstate)):
         if t is not None:
             _expect(what, name, t, (dims.b, dims.H, dims.N, dims.P), torch.float32, dev)
-    with _on_stream(dev, stream):
-        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-               "dstate0": torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)}
-        n = m3_linattn_bwd_workspace_size(dims)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        m3_linattn_bwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state0, dy, dstate,
-                       out["dq"], out["dk"], out["dv"], out["dstate0"], ws)
+    raw = _call_stream(dev.index, stream)
+    if raw is None:
+        with _elsewhere(dev, stream):
+            return linattn_backward(q, k, v, log_decay, dy, scale, lens, state0, dstate)
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+           "dstate0": torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)}
+    n = m3_linattn_bwd_workspace_size(dims)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _check(lib().m3_linattn_bwd(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                dims.N ** -0.5 if scale is None else scale, _adr(lens), _adr(state0), dy.data_ptr(),
+                                _adr(dstate), *[out[g].data_ptr() for g in ("dq", "dk", "dv", "dstate0")], _adr(ws), n,
+                                raw), "m3_linattn_bwd")
     return out
 
 
@@ -479,7 +507,7 @@ class Pages:
         if live is None:
             live = torch.zeros(self.npages, dtype=torch.int32, device=self.device)
         _expect("Pages", "live", live, (self.npages,), torch.int32, self.device)
-        self.bufs, self.live, self.struct = bufs, live, s
+        self.bufs, self.live, self.struct, self._ref = bufs, live, s, ctypes.byref(s)
 
     def _list(self, what, name, t):
         import torch
@@ -493,37 +521,49 @@ class Pages:
         n = self._list("Pages.copy", "src", src)
         if self._list("Pages.copy", "dst", dst) != n:
             raise M3Error(-1, "Pages.copy: src and dst have different lengths")
-        with _on_stream(self.device, stream):
-            _check(lib().m3_pages_copy(ctypes.byref(self.struct), n, _ptr(src), _ptr(dst), _stream()), "m3_pages_copy")
+        raw = _call_stream(self.device.index, stream)
+        if raw is None:
+            with _elsewhere(self.device, stream):
+                return self.copy(src, dst)
+        _check(lib().m3_pages_copy(self._ref, n, src.data_ptr(), dst.data_ptr(), raw), "m3_pages_copy")
 
     def fork(self, src, stream=None):
         """Take a free page for each entry and make it a copy of page src[i], or all zero where src[i]
         is negative (m3_pages_fork).  Returns the pages taken, (n) int32."""
         import torch
         n = self._list("Pages.fork", "src", src)
-        with _on_stream(self.device, stream):
-            dst = torch.empty_like(src)
-            _check(lib().m3_pages_fork(ctypes.byref(self.struct), _ptr(self.live), n, _ptr(src), _ptr(dst), _stream()),
-                   "m3_pages_fork")
+        raw = _call_stream(self.device.index, stream)
+        if raw is None:
+            with _elsewhere(self.device, stream):
+                return self.fork(src)
+        dst = torch.empty_like(src)
+        _check(lib().m3_pages_fork(self._ref, self.live.data_ptr(), n, src.data_ptr(), dst.data_ptr(), raw),
+               "m3_pages_fork")
         return dst
 
     def free(self, idx, stream=None):
         """The pages idx become free (m3_pages_free)."""
         n = self._list("Pages.free", "idx", idx)
-        with _on_stream(self.device, stream):
-            _check(lib().m3_pages_free(ctypes.byref(self.struct), _ptr(self.live), n, _ptr(idx), _stream()),
-                   "m3_pages_free")
+        raw = _call_stream(self.device.index, stream)
+        if raw is None:
+            with _elsewhere(self.device, stream):
+                return self.free(idx)
+        _check(lib().m3_pages_free(self._ref, self.live.data_ptr(), n, idx.data_ptr(), raw), "m3_pages_free")
 
     def compact(self, stream=None):
         """Move the live pages to the front, in order (m3_pages_compact).  Returns (map, count): map
         (npages) int32 says where each page went (-1: it was free), count (1) int32 how many are live."""
         import torch
-        with _on_stream(self.device, stream):
-            out = torch.empty((2 * self.npages + 2,), dtype=torch.int32, device=self.device)
-            where, order, count = out[:self.npages], out[self.npages:2 * self.npages], out[2 * self.npages:]
-            _check(lib().m3_pages_compact(ctypes.byref(self.struct), _ptr(self.live), _ptr(where), _ptr(order),
-                                          _ptr(count), _stream()), "m3_pages_compact")
-        return where, count[:1]
+        raw = _call_stream(self.device.index, stream)
+        if raw is None:
+            with _elsewhere(self.device, stream):
+                return self.compact()
+        n = self.npages
+        out = torch.empty((2 * n + 2,), dtype=torch.int32, device=self.device)  # map, order, count
+        at = out.data_ptr()
+        _check(lib().m3_pages_compact(self._ref, self.live.data_ptr(), at, at + 4 * n, at + 8 * n, raw),
+               "m3_pages_compact")
+        return out[:n], out[2 * n:2 * n + 1]
 
 
 def m3_check(stream=None) -> int:
