@@ -323,68 +323,76 @@ __global__ void __launch_bounds__(256) la_head_sum_kernel(int64_t n4, int H, int
   }
 }
 
-// One token: S <- g S + k v^T, y = scale S^T q.  A CTA takes 32 columns of one (row, head) state:
-// eight lanes read 128 bytes of a state row, sixteen row groups share the column sums.  Bound by HBM:
-// the state is read and written once.
-constexpr int kStepCols = 32, kStepThreads = 128;
+// One token: S <- g S + k v^T, y = scale S^T q.  A CTA takes COLS columns of one (row, head) state:
+// COLS / 4 lanes read a state row's segment, the other threads share the rows, and the column sums meet in
+// shared memory.  Bound by HBM: the state is read and written once.  The state's loads are issued
+// before the page is checked against the earlier rows' (the check decides what is stored, not what is
+// read), and marked as streaming: b128 H32 N = P = 128 takes 86 us (6.3 TB/s, 96 % of the measured copy
+// rate), 94 without the mark, 98 with the check first; b1 2.1 us and 3.9 with the check first.
+constexpr int kStepThreads = 128;
 
-template <bool BF16, int ITER>
+template <bool BF16, int ITER, int COLS>
 __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, int tiles) {
-  __shared__ float4 part[4][8];
-  const int tid = threadIdx.x, c4 = tid & 7, rg = tid >> 3, warp = tid >> 5, lane = tid & 31;
+  constexpr int LC = COLS / 4, RG = kStepThreads / LC;  // lanes of a row segment, row groups
+  __shared__ float4 part[4][LC];
+  const int tid = threadIdx.x, c4 = tid % LC, rg = tid / LC, warp = tid >> 5, lane = tid & 31;
   int64_t blk = blockIdx.x;
   const int tile = (int)(blk % tiles);
   const int64_t bh = blk / tiles;
   const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
-  const int p0 = tile * kStepCols + 4 * c4;
+  const int p0 = tile * COLS + 4 * c4;
   const bool on = p0 < a.P;
-  const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
+  const int64_t page = a.pages ? a.pages[bi] : bi;
+  const bool there = page >= 0 && (!a.pages || page < a.npages);
+  float* S = a.state + (page * a.H + h) * (int64_t)a.N * a.P + p0;
+  float4 s[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int n = rg + RG * i;
+    s[i] = (on && there && n < a.N) ? __ldcs(reinterpret_cast<const float4*>(S + (int64_t)n * a.P)) : make_float4(0, 0, 0, 0);
+  }
   const int64_t yi = bh * a.P + p0;
-  if (page < 0) {
+  const int64_t kq = ((int64_t)bi * a.G + h / (a.H / a.G)) * a.N;
+  float v[4], k[ITER], q[ITER];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = on ? load_in<BF16>(a.v, yi + c) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int n = rg + RG * i;
+    k[i] = n < a.N ? load_in<BF16>(a.k, kq + n) : 0.0f;
+    q[i] = n < a.N ? load_in<BF16>(a.q, kq + n) : 0.0f;
+  }
+  const float g = (float)la_pow(a.log_decay[h], 1);
+  if (a.pages && la_page_block(a.pages, a.npages, bi, a.status) < 0) {
     if (on && rg == 0)
 #pragma unroll
       for (int c = 0; c < 4; ++c) store_out<BF16>(a.y, yi + c, 0.0f);
     return;
   }
-  float* S = a.state + (page * a.H + h) * (int64_t)a.N * a.P + p0;
-  float4 s[ITER];
-#pragma unroll
-  for (int i = 0; i < ITER; ++i) {
-    const int n = rg + 16 * i;
-    s[i] = (on && n < a.N) ? *reinterpret_cast<const float4*>(S + (int64_t)n * a.P) : make_float4(0, 0, 0, 0);
-  }
-  const float g = (float)la_pow(a.log_decay[h], 1);
-  float v[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) v[c] = on ? load_in<BF16>(a.v, yi + c) : 0.0f;
-  const int64_t kq = ((int64_t)bi * a.G + h / (a.H / a.G)) * a.N;
   float4 y = make_float4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    const int n = rg + 16 * i;
-    if (n < a.N) {
-      const float k = load_in<BF16>(a.k, kq + n), q = load_in<BF16>(a.q, kq + n);
-      s[i].x = fmaf(g, s[i].x, k * v[0]);
-      s[i].y = fmaf(g, s[i].y, k * v[1]);
-      s[i].z = fmaf(g, s[i].z, k * v[2]);
-      s[i].w = fmaf(g, s[i].w, k * v[3]);
-      if (on) *reinterpret_cast<float4*>(S + (int64_t)n * a.P) = s[i];
-      y.x = fmaf(q, s[i].x, y.x);
-      y.y = fmaf(q, s[i].y, y.y);
-      y.z = fmaf(q, s[i].z, y.z);
-      y.w = fmaf(q, s[i].w, y.w);
-    }
+    const int n = rg + RG * i;
+    s[i].x = fmaf(g, s[i].x, k[i] * v[0]);
+    s[i].y = fmaf(g, s[i].y, k[i] * v[1]);
+    s[i].z = fmaf(g, s[i].z, k[i] * v[2]);
+    s[i].w = fmaf(g, s[i].w, k[i] * v[3]);
+    if (on && n < a.N) __stcs(reinterpret_cast<float4*>(S + (int64_t)n * a.P), s[i]);
+    y.x = fmaf(q[i], s[i].x, y.x);
+    y.y = fmaf(q[i], s[i].y, y.y);
+    y.z = fmaf(q[i], s[i].z, y.z);
+    y.w = fmaf(q[i], s[i].w, y.w);
   }
 #pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {
+  for (int o = LC; o < 32; o <<= 1) {
     y.x += __shfl_xor_sync(kFull, y.x, o);
     y.y += __shfl_xor_sync(kFull, y.y, o);
     y.z += __shfl_xor_sync(kFull, y.z, o);
     y.w += __shfl_xor_sync(kFull, y.w, o);
   }
-  if (lane < 8) part[warp][lane] = y;
+  if (lane < LC) part[warp][lane] = y;
   __syncthreads();
-  if (tid < 8 && on) {
+  if (tid < LC && on) {
     float o[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -463,13 +471,13 @@ cudaError_t launch_core_type(const LaCore& a, cudaStream_t stream) {
   }
 }
 
-template <int ITER>
-cudaError_t launch_step_iter(const LaStep& a, cudaStream_t stream) {
-  const int tiles = (a.P + kStepCols - 1) / kStepCols;
+template <int ITER, int COLS>
+cudaError_t launch_step_cfg(const LaStep& a, cudaStream_t stream) {
+  const int tiles = (a.P + COLS - 1) / COLS;
   const int64_t grid = a.b * a.H * tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (a.bf16) la_step_kernel<true, ITER><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
-  else la_step_kernel<false, ITER><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
+  if (a.bf16) la_step_kernel<true, ITER, COLS><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
+  else la_step_kernel<false, ITER, COLS><<<(unsigned)grid, kStepThreads, 0, stream>>>(a, tiles);
   return cudaGetLastError();
 }
 
@@ -502,10 +510,16 @@ cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, cons
   return cudaGetLastError();
 }
 
+// Columns of a CTA: 32, twice as many with at most 64 rows once that still gives every SM four CTAs (half the CTAs,
+// the same bytes in flight each; b61 H24 N = P = 64: 7.0 us against 7.8; b1 H32 N = P = 128 with 32: 2.1 us against
+// 2.6 with 64).
 cudaError_t launch_la_step(const LaStep& a, cudaStream_t stream) {
-  if (a.N <= 64) return launch_step_iter<4>(a, stream);
-  if (a.N <= 128) return launch_step_iter<8>(a, stream);
-  return launch_step_iter<16>(a, stream);
+  if (a.N <= 64) {
+    if (a.b * a.H * ((a.P + 63) / 64) >= 4 * (int64_t)sm_count()) return launch_step_cfg<8, 64>(a, stream);
+    return launch_step_cfg<4, 32>(a, stream);
+  }
+  if (a.N <= 128) return launch_step_cfg<8, 32>(a, stream);
+  return launch_step_cfg<16, 32>(a, stream);
 }
 
 }  // namespace m3
