@@ -1,13 +1,16 @@
 // m3_linattn.cu -- linear attention with a decay per head: the recurrent core for every type and
 // size (m3_linattn.cuh), the sum over a group's heads, and the one-token step.
 //
-// The core walks a sequence token by token with the state in registers: a thread holds 16 rows x
-// 4 columns of S as packed fp32 row pairs (f32x2), so a token costs three packed operations per two
+// The core walks a sequence token by token with the state in registers: a thread holds 8 rows x 4
+// columns of S as packed fp32 row pairs (f32x2), so a token costs three packed operations per two
 // state elements (k v, the decayed update, the readout) and the operand rows come from shared
-// memory as broadcast 128-bit loads.  LN = KD / 16 lanes share a column, their readouts are summed
-// by a shuffle reduce-scatter.  It is bound by the fp32 pipe: 6 KD VD flops a token and head.
+// memory as broadcast 128-bit loads.  LN = KD / 8 lanes share a column, their readouts are summed
+// by a shuffle reduce-scatter.  It is bound by the latency of a token's chain (loads, updates,
+// shuffles) at few warps and by the fp32 pipe, 6 KD VD flops a token and head, at many.  (16 rows a
+// thread took 168 registers: 97 us against FWDUS at b5 L1037 H6 N40 P56.)
 // Few sequences are cut into segments: every segment but the last is walked from a zero start (MODE 1)
-// and leaves its end state; the full pass folds the earlier segments' states into its entering state.
+// and leaves its end state, a prefix pass turns the end states into entering states, and the full pass
+// starts from those.
 //
 // g itself is rounded to fp32, and a product of d of them is off by up to d 2^-25: every 16 tokens
 // the state is multiplied by e^{16 log_decay} / g^16, taken in 64 bits, which leaves at most the
@@ -19,7 +22,7 @@ namespace m3 {
 namespace {
 
 constexpr int kTB = 16;       // tokens staged at once
-constexpr int kLaWarps = 4;
+constexpr int kLaWarps = 8;   // warps of a CTA at most
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -40,31 +43,16 @@ __device__ __forceinline__ float4 row4(const void* p, int i) {
   }
 }
 
-// Tokens of segment m: [lo, hi) of the padded sequence, and how many of them are valid.
-struct SegSpan {
-  int64_t lo, hi, ta, tb;
-};
-__device__ __forceinline__ SegSpan la_span(const LaCore& a, int m, int64_t len) {
-  SegSpan s;
-  const int64_t p0 = (int64_t)m * a.seg_tok, p1 = p0 + a.seg_tok < a.L ? p0 + a.seg_tok : a.L;
-  s.lo = a.rev ? a.L - p1 : p0;
-  s.hi = a.rev ? a.L - p0 : p1;
-  if (s.hi < s.lo) s.hi = s.lo;
-  s.ta = s.lo < len ? s.lo : len;
-  s.tb = s.hi < len ? s.hi : len;
-  return s;
-}
-
 template <bool BF16, bool OUT_F32, int LN, int MODE>
-__global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, int coltiles) {
+__global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, int coltiles, int cols) {
   constexpr bool FULL = MODE == 0;
-  constexpr int KDP = 16 * LN, CPW = 128 / LN, COLS = kLaWarps * CPW, E = BF16 ? 2 : 4;
+  constexpr int KDP = 8 * LN, CPW = 128 / LN, E = BF16 ? 2 : 4;
   using T = typename std::conditional<BF16, __nv_bfloat16, float>::type;
-  constexpr int kRow = KDP, kBuf = kTB * (2 * KDP + COLS);  // q, k, v of a token block, elements
   extern __shared__ __align__(16) uint8_t sm[];
-  T* buf = reinterpret_cast<T*>(sm);                              // [2][kBuf]
-  float* ybuf = reinterpret_cast<float*>(sm + 2 * kBuf * E);      // [kTB][COLS]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ln = lane % LN;
+  const int bufsz = kTB * (2 * KDP + cols);                   // q, k, v of a token block, elements
+  T* buf = reinterpret_cast<T*>(sm);                          // two of them
+  float* ybuf = reinterpret_cast<float*>(sm + 2 * bufsz * E);  // [kTB][cols]
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, ln = lane % LN;
   int64_t blk = blockIdx.x;
   const int ct = (int)(blk % coltiles);
   blk /= coltiles;
@@ -72,9 +60,9 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   const int seg = (int)(blk % nseg_grid);
   const int64_t bh = blk / nseg_grid;
   const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
-  const int c0 = ct * COLS;                            // first column of the block
-  const int cb = warp * CPW + (lane / LN) * 4;         // first column of the thread, within the block
-  const int ncol = a.VD - c0 < COLS ? a.VD - c0 : COLS;
+  const int c0 = ct * cols;                     // first column of the block
+  const int cb = warp * CPW + (lane / LN) * 4;  // first column of the thread, within the block
+  const int ncol = a.VD - c0 < cols ? a.VD - c0 : cols;
   const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
   const int64_t len = page < 0 ? 0 : la_len(a, bi);
   const SegSpan sp = la_span(a, seg, len);
@@ -89,66 +77,60 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   }
 
   // ---- the state entering the segment: rows 4 (ln + LN j) + e as pairs, columns cb..cb+3
-  uint64_t S[8][4];
+  uint64_t S[4][4];
   auto row_of = [&](int rp) { return 4 * (ln + LN * (rp >> 1)) + 2 * (rp & 1); };
-  auto slot = [&](int s) { return a.ws + (bh * a.nseg + s) * (int64_t)a.KD * a.VD; };
-  const int64_t sbase = (page * a.H + h) * (int64_t)a.KD * a.VD;
+  auto slot = [&](int s) { return a.ws + (bh * a.nseg + s) * (int64_t)a.KD * a.VD + c0 + cb; };
+  const int64_t sbase = (page * a.H + h) * (int64_t)a.KD * a.VD + (c0 + cb) * a.s_j;
 #pragma unroll
-  for (int rp = 0; rp < 8; ++rp)
+  for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
     for (int c = 0; c < 4; ++c) S[rp][c] = 0;
   const bool has_col = cb < ncol;  // columns come in fours: VD is a multiple of 8
+  auto put = [&](float* dst, int64_t si, int64_t sj, float f) {
+#pragma unroll
+    for (int rp = 0; rp < 4; ++rp)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int i = row_of(rp);
+        float lo, hi;
+        f2_split(S[rp][c], lo, hi);
+        if (i < a.KD) {
+          dst[i * si + c * sj] = f * lo;
+          dst[(i + 1) * si + c * sj] = f * hi;
+        }
+      }
+  };
   if (has_col && page >= 0) {
-    if (seg == 0 || !FULL) {
-      const bool from_ws = FULL && a.nseg > 1;
-      if (seg == 0 && (from_ws || a.s_in)) {
-        const float* src = from_ws ? slot(0) : a.s_in + sbase;
-        const int64_t si = from_ws ? a.VD : a.s_i, sj = from_ws ? 1 : a.s_j;
+    if (FULL && a.nseg > 1) {
+      const float* z = slot(seg);
 #pragma unroll
-        for (int rp = 0; rp < 8; ++rp)
+      for (int rp = 0; rp < 4; ++rp) {
+        const int i = row_of(rp);
+        if (i >= a.KD) continue;
+        const float4 lo = *reinterpret_cast<const float4*>(z + (int64_t)i * a.VD);
+        const float4 hi = *reinterpret_cast<const float4*>(z + (int64_t)(i + 1) * a.VD);
+        S[rp][0] = f2(lo.x, hi.x);
+        S[rp][1] = f2(lo.y, hi.y);
+        S[rp][2] = f2(lo.z, hi.z);
+        S[rp][3] = f2(lo.w, hi.w);
+      }
+    } else if (seg == 0) {
+      if (a.s_in) {
+        const float* src = a.s_in + sbase;
+#pragma unroll
+        for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int i = row_of(rp);
-            if (i < a.KD) S[rp][c] = f2(src[i * si + (c0 + cb + c) * sj], src[(i + 1) * si + (c0 + cb + c) * sj]);
+            if (i < a.KD) S[rp][c] = f2(src[i * a.s_i + c * a.s_j], src[(i + 1) * a.s_i + c * a.s_j]);
           }
       }
-      if (!FULL && seg == 0) {
-        float* w = slot(0);
-#pragma unroll
-        for (int rp = 0; rp < 8; ++rp)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = row_of(rp);
-            float lo, hi;
-            f2_split(S[rp][c], lo, hi);
-            if (i < a.KD) {
-              w[(int64_t)i * a.VD + c0 + cb + c] = lo;
-              w[(int64_t)(i + 1) * a.VD + c0 + cb + c] = hi;
-            }
-          }
-      }
-    } else {
-      for (int m = 0; m < seg; ++m) {
-        const SegSpan s = la_span(a, m, len);
-        // (against time, the sequence's first token takes the incoming state undecayed)
-        const int64_t undecayed = a.rev && s.tb == len && s.tb > s.ta;
-        const float f = (float)la_pow(ld, s.tb - s.ta - undecayed);
-        const float* z = slot(m + 1);
-#pragma unroll
-        for (int rp = 0; rp < 8; ++rp)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = row_of(rp);
-            if (i < a.KD)
-              S[rp][c] = f2_fma(S[rp][c], f2(f, f),
-                                f2(z[(int64_t)i * a.VD + c0 + cb + c], z[(int64_t)(i + 1) * a.VD + c0 + cb + c]));
-          }
-      }
+      if (!FULL) put(slot(0), a.VD, 1, 1.0f);
     }
   }
 
   // ---- token blocks, in processing order; padding rows and columns of the buffers stay zero
-  for (int i = tid; i < 2 * kBuf * E / 16; i += 32 * kLaWarps) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 2 * bufsz * E / 16; i += nthr) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   const int64_t ntok = sp.tb - sp.ta;
   const int64_t nblk = (ntok + kTB - 1) / kTB;
@@ -159,25 +141,26 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   auto stage = [&](int64_t blk_i, int s) {
     const int64_t i0 = blk_i * kTB;
     const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
-    T* bq = buf + s * kBuf;
-    T* bk = bq + kTB * kRow;
-    T* bv = bk + kTB * kRow;
-    for (int e = tid; e < nt * kc; e += 32 * kLaWarps) {
+    T* bq = buf + s * bufsz;
+    T* bk = bq + kTB * KDP;
+    T* bv = bk + kTB * KDP;
+    for (int e = tid; e < nt * kc; e += nthr) {
       const int t = e / kc, ch = e % kc;
       const int64_t row = (int64_t)bi * a.L + token(i0 + t);
       if (FULL)
-        cp_async16(bq + t * kRow + ch * (16 / E), static_cast<const T*>(a.q) + (row * a.hq + gq) * a.KD + ch * (16 / E));
-      cp_async16(bk + t * kRow + ch * (16 / E), static_cast<const T*>(a.k) + (row * a.hk + gk) * a.KD + ch * (16 / E));
+        cp_async16(bq + t * KDP + ch * (16 / E), static_cast<const T*>(a.q) + (row * a.hq + gq) * a.KD + ch * (16 / E));
+      cp_async16(bk + t * KDP + ch * (16 / E), static_cast<const T*>(a.k) + (row * a.hk + gk) * a.KD + ch * (16 / E));
     }
-    for (int e = tid; e < nt * vc; e += 32 * kLaWarps) {
+    for (int e = tid; e < nt * vc; e += nthr) {
       const int t = e / vc, ch = e % vc;
       const int64_t row = (int64_t)bi * a.L + token(i0 + t);
-      cp_async16(bv + t * COLS + ch * (16 / E),
+      cp_async16(bv + t * cols + ch * (16 / E),
                  static_cast<const T*>(a.v) + (row * a.hv + gv) * a.VD + c0 + ch * (16 / E));
     }
   };
   // against time the first token of the sequence meets the incoming state undecayed
   const bool first = a.rev && sp.tb == len;
+  const float u = a.s_upd;
   if (nblk > 0) stage(0, 0);
   cp_async_commit();
   for (int64_t ib = 0; ib < nblk; ++ib) {
@@ -188,25 +171,24 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
     __syncthreads();
     const int64_t i0 = ib * kTB;
     const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
-    const T* bq = buf + s * kBuf;
-    const T* bk = bq + kTB * kRow;
-    const T* bv = bk + kTB * kRow;
-#pragma unroll 1
+    const T* bq = buf + s * bufsz + 4 * ln;
+    const T* bk = bq + kTB * KDP;
+    const T* bv = buf + s * bufsz + 2 * kTB * KDP + cb;
+#pragma unroll 2
     for (int t = 0; t < nt; ++t) {
       const float gt = (first && ib == 0 && t == 0) ? 1.0f : g;
       const uint64_t g2 = f2(gt, gt);
-      const float4 v4 = row4<BF16>(bv + t * COLS, cb);
-      const float u = a.s_upd;
+      const float4 v4 = row4<BF16>(bv, t * cols);
       const uint64_t v2[4] = {f2(v4.x * u, v4.x * u), f2(v4.y * u, v4.y * u), f2(v4.z * u, v4.z * u),
                               f2(v4.w * u, v4.w * u)};
       uint64_t y2[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 k4 = row4<BF16>(bk + t * kRow, 4 * (ln + LN * j));
+      for (int j = 0; j < 2; ++j) {
+        const float4 k4 = row4<BF16>(bk, t * KDP + 4 * LN * j);
         const uint64_t ka = f2(k4.x, k4.y), kb = f2(k4.z, k4.w);
         uint64_t qa = 0, qb = 0;
         if (FULL) {
-          const float4 q4 = row4<BF16>(bq + t * kRow, 4 * (ln + LN * j));
+          const float4 q4 = row4<BF16>(bq, t * KDP + 4 * LN * j);
           qa = f2(q4.x, q4.y);
           qb = f2(q4.z, q4.w);
         }
@@ -215,7 +197,7 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
           S[2 * j][c] = f2_fma(S[2 * j][c], g2, f2_mul(ka, v2[c]));
           S[2 * j + 1][c] = f2_fma(S[2 * j + 1][c], g2, f2_mul(kb, v2[c]));
           if (FULL) {
-            y2[c] = f2_fma(qa, S[2 * j][c], y2[c]);
+            y2[c] = j == 0 ? f2_mul(qa, S[0][c]) : f2_fma(qa, S[2 * j][c], y2[c]);
             y2[c] = f2_fma(qb, S[2 * j + 1][c], y2[c]);
           }
         }
@@ -250,51 +232,84 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
         if (LN < 8 || (ln & (LN / 4 - 1)) == 0) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c < have) ybuf[t * COLS + cb + col + c] = a.s_out * y[c];
+            if (c < have) ybuf[t * cols + cb + col + c] = a.s_out * y[c];
         }
       }
     }
     if (nt == kTB) {
       const uint64_t c2 = f2(corr, corr);
 #pragma unroll
-      for (int rp = 0; rp < 8; ++rp)
+      for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
         for (int c = 0; c < 4; ++c) S[rp][c] = f2_mul(S[rp][c], c2);
     }
     __syncthreads();  // the block's readouts are complete, its operands read
     if constexpr (FULL) {
-      for (int e = tid; e < nt * ncol; e += 32 * kLaWarps) {
-        const int t = e / ncol, c = e % ncol;
-        store_out<!OUT_F32>(a.out, (((int64_t)bi * a.L + token(i0 + t)) * a.H + h) * a.VD + c0 + c, ybuf[t * COLS + c]);
+      const int nq = ncol / 4;
+      for (int e = tid; e < nt * nq; e += nthr) {
+        const int t = e / nq, c = 4 * (e % nq);
+        const float4 y = *reinterpret_cast<const float4*>(ybuf + t * cols + c);
+        const int64_t o = (((int64_t)bi * a.L + token(i0 + t)) * a.H + h) * a.VD + c0 + c;
+        if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = y;
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
       }
       // ybuf is rewritten after the next block's first barrier
     }
   }
   cp_async_wait<0>();
   if constexpr (FULL) {  // tokens past the sequence's length
-    for (int64_t t = sp.tb > sp.lo ? sp.tb : sp.lo; t < sp.hi; ++t)
-      for (int c = tid; c < ncol; c += 32 * kLaWarps)
-        store_out<!OUT_F32>(a.out, (((int64_t)bi * a.L + t) * a.H + h) * a.VD + c0 + c, 0.0f);
+    const int64_t z0 = sp.tb > sp.lo ? sp.tb : sp.lo;
+    const int nq = ncol / 4;
+    for (int64_t e = tid; e < (sp.hi - z0) * nq; e += nthr) {
+      const int64_t o = (((int64_t)bi * a.L + z0 + e / nq) * a.H + h) * a.VD + c0 + 4 * (e % nq);
+      if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = make_float4(0, 0, 0, 0);
+      else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(0, 0);
+    }
   }
 
   // ---- the state left behind
   if (!has_col || page < 0) return;
-  if (!FULL || (seg == a.nseg - 1 && a.s_fin)) {
-    float* dst = FULL ? a.s_fin + sbase : slot(seg + 1);
-    const int64_t si = FULL ? a.s_i : a.VD, sj = FULL ? a.s_j : 1;
-    const float f = FULL && a.rev && len > 0 ? g : 1.0f;  // against time: once more past the first token
+  if (!FULL) put(slot(seg + 1), a.VD, 1, 1.0f);
+  else if (seg == a.nseg - 1 && a.s_fin)  // against time: decayed once more past the first token
+    put(a.s_fin + sbase, a.s_i, a.s_j, a.rev && len > 0 ? g : 1.0f);
+}
+
+// The states entering the segments: slot m + 1 holds the end state of segment m from a zero start (segment 0:
+// from slot 0) and becomes the state entering segment m + 1.  One thread per four state elements, the
+// segments in order; the loads do not wait for the sums.
+__global__ void __launch_bounds__(256) la_prefix_kernel(const LaCore a, int64_t n4, int tc) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const int64_t per = (int64_t)a.KD * a.VD / 4;
+  const int64_t bh = i / per;
+  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  const int64_t len = a.pages && a.pages[bi] < 0 ? 0 : la_len(a, bi);  // (a row without a page is not used)
+  const float ld = a.log_decay[h];
+  float4* z = reinterpret_cast<float4*>(a.ws) + (bh * a.nseg) * per + i % per;
+  const float full = (float)la_pow(ld, a.seg_tok);
+  float4 s = z[per];
+  constexpr int U = 4;
+  for (int m0 = 1; m0 < a.nseg - 1; m0 += U) {
+    float4 v[U];
 #pragma unroll
-    for (int rp = 0; rp < 8; ++rp)
+    for (int u = 0; u < U; ++u)
+      if (m0 + u < a.nseg - 1) v[u] = z[(m0 + u + 1) * per];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int i = row_of(rp);
-        float lo, hi;
-        f2_split(S[rp][c], lo, hi);
-        if (i < a.KD) {
-          dst[i * si + (c0 + cb + c) * sj] = f * lo;
-          dst[(i + 1) * si + (c0 + cb + c) * sj] = f * hi;
-        }
+    for (int u = 0; u < U; ++u) {
+      const int m = m0 + u;
+      if (m >= a.nseg - 1) break;
+      int64_t e;
+      if (tc) {
+        e = la_chunks(a, m, len).tokens;
+      } else {
+        const SegSpan sp = la_span(a, m, len);
+        // (against time, the sequence's first token takes the incoming state undecayed)
+        e = sp.tb - sp.ta - (a.rev && sp.tb == len && sp.tb > sp.ta);
       }
+      const float f = e == a.seg_tok ? full : (float)la_pow(ld, e);
+      s = make_float4(fmaf(f, s.x, v[u].x), fmaf(f, s.y, v[u].y), fmaf(f, s.z, v[u].z), fmaf(f, s.w, v[u].w));
+      z[(m + 1) * per] = s;
+    }
   }
 }
 
@@ -415,19 +430,26 @@ int sm_count() {
 
 int lanes_of(int KD) {
   int ln = 1;
-  while (16 * ln < KD) ln *= 2;
+  while (8 * ln < KD) ln *= 2;
   return ln;
 }
 
-int cols_of(int KD) { return kLaWarps * 128 / lanes_of(KD); }
+// Columns and warps of a CTA: the value dim over as few CTAs of at most kLaWarps warps as it takes.
+int warps_of(const LaCore& a) {
+  const int cpw = 128 / lanes_of(a.KD), need = (a.VD + cpw - 1) / cpw;
+  const int ctas = (need + kLaWarps - 1) / kLaWarps;
+  return (need + ctas - 1) / ctas;
+}
+int cols_of(const LaCore& a) { return warps_of(a) * (128 / lanes_of(a.KD)); }
 
-// Segments of a sequence: enough CTAs for three per SM (about what the registers allow), each at
-// least 64 tokens long so that the walk outweighs reading the earlier segments' states.
+// Segments of a sequence: enough for 16 warps per SM (about what the registers allow), each at
+// least 32 tokens long so that the walk outweighs reading the earlier segments' states.
 void plan_core(LaCore* a) {
   if (la_tc_supported(*a)) return la_tc_plan(a, sm_count());
-  const int64_t units = a->b * a->H * ((a->VD + cols_of(a->KD) - 1) / cols_of(a->KD));
-  int64_t nseg = units > 0 ? (int64_t)sm_count() * 3 / units : 1;
-  const int64_t most = a->L / 64;
+  const int cols = cols_of(*a);
+  const int64_t warps = a->b * a->H * ((a->VD + cols - 1) / cols) * warps_of(*a);
+  int64_t nseg = warps > 0 ? (int64_t)sm_count() * 16 / warps : 1;
+  const int64_t most = a->L / 32;
   if (nseg > most) nseg = most;
   if (nseg > 64) nseg = 64;
   if (nseg < 2) nseg = 1;
@@ -438,23 +460,24 @@ void plan_core(LaCore* a) {
 
 template <bool BF16, bool OUT_F32, int LN, int MODE>
 cudaError_t launch_core_cfg(const LaCore& a, cudaStream_t stream) {
-  constexpr int KDP = 16 * LN, COLS = kLaWarps * 128 / LN;
-  constexpr int bytes = 2 * kTB * (2 * KDP + COLS) * (BF16 ? 2 : 4) + kTB * COLS * 4;
+  const int cols = cols_of(a);
+  const int bytes = 2 * kTB * (2 * 8 * LN + cols) * (BF16 ? 2 : 4) + kTB * cols * 4;
   static SmemAttr attr;
   auto k = la_core_kernel<BF16, OUT_F32, LN, MODE>;
   const cudaError_t e = attr.ensure(k, bytes);
   if (e != cudaSuccess) return e;
-  const int tiles = (a.VD + COLS - 1) / COLS;
+  const int tiles = (a.VD + cols - 1) / cols;
   const int64_t grid = a.b * a.H * tiles * (MODE == 0 ? a.nseg : a.nseg - 1);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  k<<<(unsigned)grid, 32 * kLaWarps, bytes, stream>>>(a, tiles);
+  k<<<(unsigned)grid, 32 * warps_of(a), bytes, stream>>>(a, tiles, cols);
   return cudaGetLastError();
 }
 
 template <bool BF16, bool OUT_F32, int LN>
 cudaError_t launch_core_ln(const LaCore& a, cudaStream_t stream) {
   if (a.nseg > 1) {
-    const cudaError_t e = launch_core_cfg<BF16, BF16 ? false : true, LN, 1>(a, stream);
+    cudaError_t e = launch_core_cfg<BF16, BF16 ? false : true, LN, 1>(a, stream);
+    if (e == cudaSuccess) e = launch_la_prefix(a, false, stream);
     if (e != cudaSuccess) return e;
   }
   return launch_core_cfg<BF16, OUT_F32, LN, 0>(a, stream);
@@ -467,7 +490,8 @@ cudaError_t launch_core_type(const LaCore& a, cudaStream_t stream) {
     case 2: return launch_core_ln<BF16, OUT_F32, 2>(a, stream);
     case 4: return launch_core_ln<BF16, OUT_F32, 4>(a, stream);
     case 8: return launch_core_ln<BF16, OUT_F32, 8>(a, stream);
-    default: return launch_core_ln<BF16, OUT_F32, 16>(a, stream);
+    case 16: return launch_core_ln<BF16, OUT_F32, 16>(a, stream);
+    default: return launch_core_ln<BF16, OUT_F32, 32>(a, stream);
   }
 }
 
@@ -482,6 +506,14 @@ cudaError_t launch_step_cfg(const LaStep& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream) {
+  if (a.nseg < 3) return cudaSuccess;  // slot 1 is the end state of segment 0 already
+  const int64_t n4 = a.b * a.H * ((int64_t)a.KD * a.VD / 4), grid = (n4 + 255) / 256;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  la_prefix_kernel<<<(unsigned)grid, 256, 0, stream>>>(a, n4, tc);
+  return cudaGetLastError();
+}
 
 size_t la_core_ws_bytes(const LaCore& a0) {
   LaCore a = a0;

@@ -36,7 +36,8 @@ struct LaCore {
   int nseg;                // segments of a sequence walked in parallel
   int64_t seg_tok;         // tokens of a segment (in processing order)
   float* ws;               // (b * H, nseg, KD, VD) when nseg > 1: slot 0 the incoming state, slot m + 1
-                           // the end state of segment m from a zero start (segment 0: from slot 0)
+                           // the end state of segment m from a zero start (segment 0: from slot 0), then
+                           // the state entering segment m + 1
   int* status;
 };
 
@@ -50,6 +51,41 @@ __device__ __forceinline__ int64_t la_len(const LaCore& a, int bi) {
 // their weight to fp32 accuracy.  g = 0 (log_decay = -inf) keeps g^0 = 1.
 __device__ __forceinline__ double la_pow(float log_decay, int64_t e) {
   return e <= 0 ? 1.0 : exp((double)log_decay * (double)e);
+}
+// Tokens of segment m: [lo, hi) of the padded sequence, and how many of them are valid.
+struct SegSpan {
+  int64_t lo, hi, ta, tb;
+};
+__device__ __forceinline__ SegSpan la_span(const LaCore& a, int m, int64_t len) {
+  SegSpan s;
+  const int64_t p0 = (int64_t)m * a.seg_tok, p1 = p0 + a.seg_tok < a.L ? p0 + a.seg_tok : a.L;
+  s.lo = a.rev ? a.L - p1 : p0;
+  s.hi = a.rev ? a.L - p0 : p1;
+  if (s.hi < s.lo) s.hi = s.lo;
+  s.ta = s.lo < len ? s.lo : len;
+  s.tb = s.hi < len ? s.hi : len;
+  return s;
+}
+constexpr int kLaChunk = 128;  // tokens of a chunk of the tensor-core form
+// The valid chunks of a segment, in processing order: chunk(i), i < n; chunks [z0, z1) of it lie
+// past the sequence's length.  A segment's tokens: those that are valid.
+struct ChunkSpan {
+  int64_t first, z0, z1, tokens;
+  int n;
+};
+__device__ __forceinline__ ChunkSpan la_chunks(const LaCore& a, int seg, int64_t len) {
+  const int64_t nch = (a.L + kLaChunk - 1) / kLaChunk, segc = a.seg_tok / kLaChunk, nvc = (len + kLaChunk - 1) / kLaChunk;
+  const int64_t p0 = seg * segc < nch ? seg * segc : nch, p1 = p0 + segc < nch ? p0 + segc : nch;
+  ChunkSpan c;
+  const int64_t lo = a.rev ? nch - p1 : p0, hi = a.rev ? nch - p0 : p1;  // chunks [lo, hi)
+  const int64_t top = hi < nvc ? hi : nvc;
+  c.n = top > lo ? (int)(top - lo) : 0;
+  c.first = a.rev ? top - 1 : lo;
+  c.z0 = top > lo ? top : lo;
+  c.z1 = hi;
+  const int64_t end = top * kLaChunk < len ? top * kLaChunk : len;
+  c.tokens = c.n > 0 ? end - lo * kLaChunk : 0;
+  return c;
 }
 // The state row of batch row bi, or -1 for a row without one: a negative page (padding), a page past the
 // pool or a page that an earlier row of the batch holds already (both recorded in the status word).
@@ -68,6 +104,7 @@ __device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t n
 }
 
 // Launchers.
+cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream);  // entering states from end states
 size_t la_core_ws_bytes(const LaCore& a);  // scratch of the pass (plans its segments)
 bool la_tc_supported(const LaCore& a);     // the tensor-core form takes this pass
 void la_tc_plan(LaCore* a, int sms);

@@ -43,7 +43,7 @@
 namespace m3 {
 namespace {
 
-constexpr int LQ = 128;  // tokens of a chunk
+constexpr int LQ = kLaChunk;  // tokens of a chunk
 constexpr int LV = 64;   // value columns of a CTA
 constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2, L_SIGNAL = 3;  // L_STORE also signals the score group
 constexpr int L_CTRL = 4;       // control warps
@@ -186,27 +186,6 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void la_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The valid chunks of a segment, in processing order: chunk(i), i < n; chunks [z0, z1) of it lie
-// past the sequence's length.  A segment's tokens: those that are valid.
-struct ChunkSpan {
-  int64_t first, z0, z1, tokens;
-  int n;
-};
-__device__ __forceinline__ ChunkSpan la_chunks(const LaCore& a, int seg, int64_t len) {
-  const int64_t nch = (a.L + LQ - 1) / LQ, segc = a.seg_tok / LQ, nvc = (len + LQ - 1) / LQ;
-  const int64_t p0 = seg * segc < nch ? seg * segc : nch, p1 = p0 + segc < nch ? p0 + segc : nch;
-  ChunkSpan c;
-  const int64_t lo = a.rev ? nch - p1 : p0, hi = a.rev ? nch - p0 : p1;  // chunks [lo, hi)
-  const int64_t top = hi < nvc ? hi : nvc;
-  c.n = top > lo ? (int)(top - lo) : 0;
-  c.first = a.rev ? top - 1 : lo;
-  c.z0 = top > lo ? top : lo;
-  c.z1 = hi;
-  const int64_t end = top * LQ < len ? top * LQ : len;
-  c.tokens = c.n > 0 ? end - lo * LQ : 0;
-  return c;
 }
 
 template <int KD, int MODE>
@@ -597,27 +576,14 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       }
     };
     if (owner && page >= 0) {
-      if (seg == 0) {
-        const bool from_ws = FULL && a.nseg > 1;
-        if (from_ws || a.s_in) {
-          const float* src = from_ws ? slot(0) : a.s_in + sbase;
-          const int64_t sj = from_ws ? 1 : a.s_j;
+      const bool from_ws = FULL && a.nseg > 1;
+      if (from_ws || (seg == 0 && a.s_in)) {
+        const float* src = from_ws ? slot(seg) : a.s_in + sbase;
+        const int64_t sj = from_ws ? 1 : a.s_j;
 #pragma unroll
-          for (int e = 0; e < LSC / 2; ++e) S[e] = f2(src[2 * e * sj], src[(2 * e + 1) * sj]);
-        }
-        if (!FULL) store_slot(0);
-      } else if (FULL) {
-        for (int m = 0; m < seg; ++m) {
-          const float f = (float)la_pow(ld, la_chunks(a, m, len).tokens);
-          const float4* z = reinterpret_cast<const float4*>(slot(m + 1));
-#pragma unroll
-          for (int e = 0; e < LSC / 4; ++e) {
-            const float4 v = z[e];
-            S[2 * e] = f2_fma(f2(f, f), S[2 * e], f2(v.x, v.y));
-            S[2 * e + 1] = f2_fma(f2(f, f), S[2 * e + 1], f2(v.z, v.w));
-          }
-        }
+        for (int e = 0; e < LSC / 2; ++e) S[e] = f2(src[2 * e * sj], src[(2 * e + 1) * sj]);
       }
+      if (!FULL && seg == 0) store_slot(0);
     }
     auto publish = [&]() {  // bf16(S), the B operand of Yi
       if (owner) {
@@ -793,7 +759,8 @@ cudaError_t launch_tc_kd(const LaCore& a, cudaStream_t stream) {
   if (a.out_f32) o = v;  // unused: fp32 outputs are written from registers
   else if (!la_map(&o, a, a.out, a.H, a.VD)) return cudaErrorInvalidValue;
   if (a.nseg > 1) {
-    const cudaError_t e = launch_tc_mode<KD, 1>(q, k, v, o, a, stream);
+    cudaError_t e = launch_tc_mode<KD, 1>(q, k, v, o, a, stream);
+    if (e == cudaSuccess) e = launch_la_prefix(a, true, stream);
     if (e != cudaSuccess) return e;
   }
   return launch_tc_mode<KD, 0>(q, k, v, o, a, stream);
