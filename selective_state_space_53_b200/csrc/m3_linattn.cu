@@ -22,6 +22,7 @@ namespace m3 {
 namespace {
 
 constexpr int kTB = 16;       // tokens staged at once
+constexpr int kMaxSeg = 64;   // segments of a sequence at most
 constexpr int kLaWarps = 8;   // warps of a CTA at most
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -53,40 +54,42 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   T* buf = reinterpret_cast<T*>(sm);                          // two of them
   float* ybuf = reinterpret_cast<float*>(sm + 2 * bufsz * E);  // [kTB][cols]
   const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31, ln = lane % LN;
-  int64_t blk = blockIdx.x;
-  const int ct = (int)(blk % coltiles);
-  blk /= coltiles;
-  const int nseg_grid = FULL ? a.nseg : a.nseg - 1;
+  unsigned blk = blockIdx.x;
+  const int ct = (int)(blk % (unsigned)coltiles);
+  blk /= (unsigned)coltiles;
+  const unsigned nseg_grid = FULL ? a.nseg : a.nseg - 1;
   const int seg = (int)(blk % nseg_grid);
-  const int64_t bh = blk / nseg_grid;
-  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  const int bh = (int)(blk / nseg_grid);
+  const int bi = bh / a.H, h = bh % a.H;
   const int c0 = ct * cols;                     // first column of the block
   const int cb = warp * CPW + (lane / LN) * 4;  // first column of the thread, within the block
   const int ncol = a.VD - c0 < cols ? a.VD - c0 : cols;
   const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
-  const int64_t len = page < 0 ? 0 : la_len(a, bi);
+  const int len = page < 0 ? 0 : la_len(a, bi);
   const SegSpan sp = la_span(a, seg, len);
   const float ld = a.log_decay[h];
-  const float g = (float)la_pow(ld, 1);
-  float corr = 1.0f;
-  {
-    double gp = (double)g;
+  // g and e^{16 log_decay} / g^16, by one warp (64-bit exponentials are slow to issue)
+  __shared__ float factors[2];
+  if (warp == 0) {
+    const double w = la_pow(ld, lane == 0 ? 1 : kTB);
+    double gp = (double)(float)__shfl_sync(kFull, w, 0);
+    if (lane == 0) factors[0] = (float)w;
 #pragma unroll
     for (int i = 1; i < kTB; i *= 2) gp *= gp;
-    if (gp > 1e-30) corr = (float)(la_pow(ld, kTB) / gp);
+    if (lane == 1) factors[1] = gp > 1e-30 ? (float)(w / gp) : 1.0f;
   }
 
   // ---- the state entering the segment: rows 4 (ln + LN j) + e as pairs, columns cb..cb+3
   uint64_t S[4][4];
   auto row_of = [&](int rp) { return 4 * (ln + LN * (rp >> 1)) + 2 * (rp & 1); };
-  auto slot = [&](int s) { return a.ws + (bh * a.nseg + s) * (int64_t)a.KD * a.VD + c0 + cb; };
-  const int64_t sbase = (page * a.H + h) * (int64_t)a.KD * a.VD + (c0 + cb) * a.s_j;
+  auto slot = [&](int s) { return a.ws + ((int64_t)bh * a.nseg + s) * (a.KD * a.VD) + c0 + cb; };
+  const int64_t sbase = (page * a.H + h) * (a.KD * a.VD) + (c0 + cb) * a.s_j;
 #pragma unroll
   for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
     for (int c = 0; c < 4; ++c) S[rp][c] = 0;
   const bool has_col = cb < ncol;  // columns come in fours: VD is a multiple of 8
-  auto put = [&](float* dst, int64_t si, int64_t sj, float f) {
+  auto put = [&](float* dst, int si, int sj, float f) {  // within one state: 32-bit offsets
 #pragma unroll
     for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
@@ -117,12 +120,13 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
     } else if (seg == 0) {
       if (a.s_in) {
         const float* src = a.s_in + sbase;
+        const int si = (int)a.s_i, sj = (int)a.s_j;
 #pragma unroll
         for (int rp = 0; rp < 4; ++rp)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int i = row_of(rp);
-            if (i < a.KD) S[rp][c] = f2(src[i * a.s_i + c * a.s_j], src[(i + 1) * a.s_i + c * a.s_j]);
+            if (i < a.KD) S[rp][c] = f2(src[i * si + c * sj], src[(i + 1) * si + c * sj]);
           }
       }
       if (!FULL) put(slot(0), a.VD, 1, 1.0f);
@@ -130,32 +134,36 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   }
 
   // ---- token blocks, in processing order; padding rows and columns of the buffers stay zero
-  for (int i = tid; i < 2 * bufsz * E / 16; i += nthr) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+  if (a.KD < KDP || ncol < cols)
+    for (int i = tid; i < 2 * bufsz * E / 16; i += nthr) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const int64_t ntok = sp.tb - sp.ta;
-  const int64_t nblk = (ntok + kTB - 1) / kTB;
+  const float g = factors[0], corr = factors[1];
+  const int ntok = sp.tb - sp.ta;
+  const int nblk = (ntok + kTB - 1) / kTB;
   const int gq = h / (a.H / a.hq), gk = h / (a.H / a.hk), gv = h / (a.H / a.hv);
   // token of position i of the segment
-  auto token = [&](int64_t i) { return a.rev ? sp.tb - 1 - i : sp.ta + i; };
+  auto token = [&](int i) { return a.rev ? sp.tb - 1 - i : sp.ta + i; };
   const int kc = a.KD * E / 16, vc = ncol * E / 16;  // 16-byte chunks of a row
-  auto stage = [&](int64_t blk_i, int s) {
-    const int64_t i0 = blk_i * kTB;
-    const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
+  // A thread copies chunk lane & 15 (+ 16 j) of the rows warp * 2 + (lane >> 4) + 2 warps * i of a block.
+  const int sl = lane & 15, sr = 2 * warp + (lane >> 4), sstep = nthr >> 4;
+  const T* qg = static_cast<const T*>(a.q) + ((int64_t)bi * a.L * a.hq + gq) * a.KD;
+  const T* kg = static_cast<const T*>(a.k) + ((int64_t)bi * a.L * a.hk + gk) * a.KD;
+  const T* vg = static_cast<const T*>(a.v) + ((int64_t)bi * a.L * a.hv + gv) * a.VD + c0;
+  const int64_t qs = (int64_t)a.hq * a.KD, ks = (int64_t)a.hk * a.KD, vs = (int64_t)a.hv * a.VD;
+  constexpr int CE = 16 / E;  // elements of a chunk
+  auto stage = [&](int blk_i, int s) {
+    const int i0 = blk_i * kTB;
+    const int nt = ntok - i0 < kTB ? ntok - i0 : kTB;
     T* bq = buf + s * bufsz;
     T* bk = bq + kTB * KDP;
     T* bv = bk + kTB * KDP;
-    for (int e = tid; e < nt * kc; e += nthr) {
-      const int t = e / kc, ch = e % kc;
-      const int64_t row = (int64_t)bi * a.L + token(i0 + t);
-      if (FULL)
-        cp_async16(bq + t * KDP + ch * (16 / E), static_cast<const T*>(a.q) + (row * a.hq + gq) * a.KD + ch * (16 / E));
-      cp_async16(bk + t * KDP + ch * (16 / E), static_cast<const T*>(a.k) + (row * a.hk + gk) * a.KD + ch * (16 / E));
-    }
-    for (int e = tid; e < nt * vc; e += nthr) {
-      const int t = e / vc, ch = e % vc;
-      const int64_t row = (int64_t)bi * a.L + token(i0 + t);
-      cp_async16(bv + t * cols + ch * (16 / E),
-                 static_cast<const T*>(a.v) + (row * a.hv + gv) * a.VD + c0 + ch * (16 / E));
+    for (int t = sr; t < nt; t += sstep) {
+      const int64_t tok = token(i0 + t);
+      for (int ch = sl; ch < kc; ch += 16) {
+        if (FULL) cp_async16(bq + t * KDP + ch * CE, qg + tok * qs + ch * CE);
+        cp_async16(bk + t * KDP + ch * CE, kg + tok * ks + ch * CE);
+      }
+      for (int ch = sl; ch < vc; ch += 16) cp_async16(bv + t * cols + ch * CE, vg + tok * vs + ch * CE);
     }
   };
   // against time the first token of the sequence meets the incoming state undecayed
@@ -163,25 +171,25 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
   const float u = a.s_upd;
   if (nblk > 0) stage(0, 0);
   cp_async_commit();
-  for (int64_t ib = 0; ib < nblk; ++ib) {
-    const int s = (int)(ib & 1);
+  for (int ib = 0; ib < nblk; ++ib) {
+    const int s = ib & 1;
     if (ib + 1 < nblk) stage(ib + 1, s ^ 1);
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
-    const int64_t i0 = ib * kTB;
-    const int nt = ntok - i0 < kTB ? (int)(ntok - i0) : kTB;
+    const int i0 = ib * kTB;
+    const int nt = ntok - i0 < kTB ? ntok - i0 : kTB;
     const T* bq = buf + s * bufsz + 4 * ln;
     const T* bk = bq + kTB * KDP;
     const T* bv = buf + s * bufsz + 2 * kTB * KDP + cb;
-#pragma unroll 2
-    for (int t = 0; t < nt; ++t) {
+    // one token: the state's update, and this thread's share of the four readouts
+    auto walk = [&](int t, float (&y)[4]) {
       const float gt = (first && ib == 0 && t == 0) ? 1.0f : g;
       const uint64_t g2 = f2(gt, gt);
       const float4 v4 = row4<BF16>(bv, t * cols);
       const uint64_t v2[4] = {f2(v4.x * u, v4.x * u), f2(v4.y * u, v4.y * u), f2(v4.z * u, v4.z * u),
                               f2(v4.w * u, v4.w * u)};
-      uint64_t y2[4] = {0, 0, 0, 0};
+      uint64_t ya[4], yb[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float4 k4 = row4<BF16>(bk, t * KDP + 4 * LN * j);
@@ -196,44 +204,68 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
         for (int c = 0; c < 4; ++c) {
           S[2 * j][c] = f2_fma(S[2 * j][c], g2, f2_mul(ka, v2[c]));
           S[2 * j + 1][c] = f2_fma(S[2 * j + 1][c], g2, f2_mul(kb, v2[c]));
-          if (FULL) {
-            y2[c] = j == 0 ? f2_mul(qa, S[0][c]) : f2_fma(qa, S[2 * j][c], y2[c]);
-            y2[c] = f2_fma(qb, S[2 * j + 1][c], y2[c]);
+          if (FULL) {  // two short chains
+            ya[c] = j == 0 ? f2_mul(qa, S[2 * j][c]) : f2_fma(qa, S[2 * j][c], ya[c]);
+            yb[c] = j == 0 ? f2_mul(qb, S[2 * j + 1][c]) : f2_fma(qb, S[2 * j + 1][c], yb[c]);
           }
         }
       }
       if constexpr (FULL) {
-        float y[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float lo, hi;
-          f2_split(y2[c], lo, hi);
-          y[c] = lo + hi;
+          float a0, a1, b0, b1;
+          f2_split(ya[c], a0, a1);
+          f2_split(yb[c], b0, b1);
+          y[c] = (a0 + a1) + (b0 + b1);
         }
-        // sum over the LN lanes of a column: two halving exchanges, then plain butterflies
-        int col = 0, have = 4;
-        if constexpr (LN >= 2) {
-          const bool up = ln & (LN / 2);
-          const float s0 = up ? y[0] : y[2], s1 = up ? y[1] : y[3];
-          y[0] = (up ? y[2] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 2);
-          y[1] = (up ? y[3] : y[1]) + __shfl_xor_sync(kFull, s1, LN / 2);
-          col = up ? 2 : 0;
-          have = 2;
-        }
-        if constexpr (LN >= 4) {
-          const bool up = ln & (LN / 4);
-          const float s0 = up ? y[0] : y[1];
-          y[0] = (up ? y[1] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 4);
-          col += up ? 1 : 0;
-          have = 1;
-        }
+      }
+    };
+    // sum over the LN lanes of a column, two halving exchanges, then plain butterflies; lane ln then holds
+    // `have` columns from `col`
+    constexpr int have = LN >= 4 ? 1 : LN == 2 ? 2 : 4;
+    const int col = (LN >= 2 && (ln & (LN / 2)) ? 2 : 0) + (LN >= 4 && (ln & (LN / 4)) ? 1 : 0);
+    auto reduce = [&](float (&y)[4]) {
+      if constexpr (LN >= 2) {
+        const bool up = ln & (LN / 2);
+        const float s0 = up ? y[0] : y[2], s1 = up ? y[1] : y[3];
+        y[0] = (up ? y[2] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 2);
+        y[1] = (up ? y[3] : y[1]) + __shfl_xor_sync(kFull, s1, LN / 2);
+      }
+      if constexpr (LN >= 4) {
+        const bool up = ln & (LN / 4);
+        const float s0 = up ? y[0] : y[1];
+        y[0] = (up ? y[1] : y[0]) + __shfl_xor_sync(kFull, s0, LN / 4);
+      }
 #pragma unroll
-        for (int o = LN / 8; o > 0; o >>= 1) y[0] += __shfl_xor_sync(kFull, y[0], o);
-        if (LN < 8 || (ln & (LN / 4 - 1)) == 0) {
+      for (int o = LN / 8; o > 0; o >>= 1) y[0] += __shfl_xor_sync(kFull, y[0], o);
+    };
+    auto keep = [&](int t, const float (&y)[4]) {
+      if (LN < 8 || (ln & (LN / 4 - 1)) == 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c < have) ybuf[t * cols + cb + col + c] = a.s_out * y[c];
-        }
+        for (int c = 0; c < have; ++c) ybuf[t * cols + cb + col + c] = a.s_out * y[c];
+      }
+    };
+    // four tokens at a time: their sums over the lanes overlap (one by one a token took 400 cycles)
+    int t = 0;
+#pragma unroll 1
+    for (; t + 4 <= nt; t += 4) {
+      float y[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) walk(t + i, y[i]);
+      if constexpr (FULL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reduce(y[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) keep(t + i, y[i]);
+      }
+    }
+#pragma unroll 1
+    for (; t < nt; ++t) {
+      float y[4];
+      walk(t, y);
+      if constexpr (FULL) {
+        reduce(y);
+        keep(t, y);
       }
     }
     if (nt == kTB) {
@@ -245,70 +277,69 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
     }
     __syncthreads();  // the block's readouts are complete, its operands read
     if constexpr (FULL) {
-      const int nq = ncol / 4;
-      for (int e = tid; e < nt * nq; e += nthr) {
-        const int t = e / nq, c = 4 * (e % nq);
-        const float4 y = *reinterpret_cast<const float4*>(ybuf + t * cols + c);
-        const int64_t o = (((int64_t)bi * a.L + token(i0 + t)) * a.H + h) * a.VD + c0 + c;
-        if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = y;
-        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-      }
+      for (int t = sr; t < nt; t += sstep)
+        for (int c = 4 * sl; c < ncol; c += 64) {
+          const float4 y = *reinterpret_cast<const float4*>(ybuf + t * cols + c);
+          const int64_t o = (((int64_t)bi * a.L + token(i0 + t)) * a.H + h) * a.VD + c0 + c;
+          if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = y;
+          else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        }
       // ybuf is rewritten after the next block's first barrier
     }
   }
   cp_async_wait<0>();
   if constexpr (FULL) {  // tokens past the sequence's length
-    const int64_t z0 = sp.tb > sp.lo ? sp.tb : sp.lo;
-    const int nq = ncol / 4;
-    for (int64_t e = tid; e < (sp.hi - z0) * nq; e += nthr) {
-      const int64_t o = (((int64_t)bi * a.L + z0 + e / nq) * a.H + h) * a.VD + c0 + 4 * (e % nq);
-      if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = make_float4(0, 0, 0, 0);
-      else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(0, 0);
-    }
+    for (int t = (sp.tb > sp.lo ? sp.tb : sp.lo) + sr; t < sp.hi; t += sstep)
+      for (int c = 4 * sl; c < ncol; c += 64) {
+        const int64_t o = (((int64_t)bi * a.L + t) * a.H + h) * a.VD + c0 + c;
+        if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = make_float4(0, 0, 0, 0);
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + o) = make_uint2(0, 0);
+      }
   }
 
   // ---- the state left behind
   if (!has_col || page < 0) return;
   if (!FULL) put(slot(seg + 1), a.VD, 1, 1.0f);
   else if (seg == a.nseg - 1 && a.s_fin)  // against time: decayed once more past the first token
-    put(a.s_fin + sbase, a.s_i, a.s_j, a.rev && len > 0 ? g : 1.0f);
+    put(a.s_fin + sbase, (int)a.s_i, (int)a.s_j, a.rev && len > 0 ? g : 1.0f);
 }
 
 // The states entering the segments: slot m + 1 holds the end state of segment m from a zero start (segment 0:
 // from slot 0) and becomes the state entering segment m + 1.  One thread per four state elements, the
 // segments in order; the loads do not wait for the sums.
-__global__ void __launch_bounds__(256) la_prefix_kernel(const LaCore a, int64_t n4, int tc) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const int64_t per = (int64_t)a.KD * a.VD / 4;
-  const int64_t bh = i / per;
-  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
-  const int64_t len = a.pages && a.pages[bi] < 0 ? 0 : la_len(a, bi);  // (a row without a page is not used)
-  const float ld = a.log_decay[h];
-  float4* z = reinterpret_cast<float4*>(a.ws) + (bh * a.nseg) * per + i % per;
-  const float full = (float)la_pow(ld, a.seg_tok);
+__global__ void __launch_bounds__(128) la_prefix_kernel(const LaCore a, int per, int tc) {
+  const int bh = blockIdx.x, e4 = blockIdx.y * 128 + threadIdx.x;
+  const int bi = bh / a.H, h = bh % a.H;
+  __shared__ float f[kMaxSeg];  // the decay over each segment
+  if (threadIdx.x < a.nseg) {
+    const int len = la_len(a, bi), m = threadIdx.x;
+    int e;
+    if (tc) {
+      e = la_chunks(a, m, len).tokens;
+    } else {
+      const SegSpan sp = la_span(a, m, len);
+      // (against time, the sequence's first token takes the incoming state undecayed)
+      e = sp.tb - sp.ta - (a.rev && sp.tb == len && sp.tb > sp.ta);
+    }
+    f[m] = (float)la_pow(a.log_decay[h], e);
+  }
+  float4* z = reinterpret_cast<float4*>(a.ws) + (int64_t)bh * a.nseg * per + e4;
+  __syncthreads();
+  if (e4 >= per) return;
   float4 s = z[per];
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (int m0 = 1; m0 < a.nseg - 1; m0 += U) {
     float4 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (m0 + u < a.nseg - 1) v[u] = z[(m0 + u + 1) * per];
+      if (m0 + u < a.nseg - 1) v[u] = z[(int64_t)(m0 + u + 1) * per];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int m = m0 + u;
-      if (m >= a.nseg - 1) break;
-      int64_t e;
-      if (tc) {
-        e = la_chunks(a, m, len).tokens;
-      } else {
-        const SegSpan sp = la_span(a, m, len);
-        // (against time, the sequence's first token takes the incoming state undecayed)
-        e = sp.tb - sp.ta - (a.rev && sp.tb == len && sp.tb > sp.ta);
+      if (m < a.nseg - 1) {
+        s = make_float4(fmaf(f[m], s.x, v[u].x), fmaf(f[m], s.y, v[u].y), fmaf(f[m], s.z, v[u].z), fmaf(f[m], s.w, v[u].w));
+        z[(int64_t)(m + 1) * per] = s;
       }
-      const float f = e == a.seg_tok ? full : (float)la_pow(ld, e);
-      s = make_float4(fmaf(f, s.x, v[u].x), fmaf(f, s.y, v[u].y), fmaf(f, s.z, v[u].z), fmaf(f, s.w, v[u].w));
-      z[(m + 1) * per] = s;
     }
   }
 }
@@ -351,10 +382,8 @@ __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, i
   constexpr int LC = COLS / 4, RG = kStepThreads / LC;  // lanes of a row segment, row groups
   __shared__ float4 part[4][LC];
   const int tid = threadIdx.x, c4 = tid % LC, rg = tid / LC, warp = tid >> 5, lane = tid & 31;
-  int64_t blk = blockIdx.x;
-  const int tile = (int)(blk % tiles);
-  const int64_t bh = blk / tiles;
-  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  const unsigned tile = blockIdx.x % (unsigned)tiles, bh = blockIdx.x / (unsigned)tiles;
+  const int bi = (int)(bh / (unsigned)a.H), h = (int)(bh % (unsigned)a.H);
   const int p0 = tile * COLS + 4 * c4;
   const bool on = p0 < a.P;
   const int64_t page = a.pages ? a.pages[bi] : bi;
@@ -366,7 +395,7 @@ __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, i
     const int n = rg + RG * i;
     s[i] = (on && there && n < a.N) ? __ldcs(reinterpret_cast<const float4*>(S + (int64_t)n * a.P)) : make_float4(0, 0, 0, 0);
   }
-  const int64_t yi = bh * a.P + p0;
+  const int64_t yi = (int64_t)bh * a.P + p0;
   const int64_t kq = ((int64_t)bi * a.G + h / (a.H / a.G)) * a.N;
   float v[4], k[ITER], q[ITER];
 #pragma unroll
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, i
     k[i] = n < a.N ? load_in<BF16>(a.k, kq + n) : 0.0f;
     q[i] = n < a.N ? load_in<BF16>(a.q, kq + n) : 0.0f;
   }
-  const float g = (float)la_pow(a.log_decay[h], 1);
+  const float g = (float)exp((double)a.log_decay[h]);
   if (a.pages && la_page_block(a.pages, a.npages, bi, a.status) < 0) {
     if (on && rg == 0)
 #pragma unroll
@@ -451,7 +480,7 @@ void plan_core(LaCore* a) {
   int64_t nseg = warps > 0 ? (int64_t)sm_count() * 16 / warps : 1;
   const int64_t most = a->L / 32;
   if (nseg > most) nseg = most;
-  if (nseg > 64) nseg = 64;
+  if (nseg > kMaxSeg) nseg = kMaxSeg;
   if (nseg < 2) nseg = 1;
   a->seg_tok = (a->L + nseg - 1) / nseg;
   if (a->seg_tok < 1) a->seg_tok = 1;
@@ -509,9 +538,8 @@ cudaError_t launch_step_cfg(const LaStep& a, cudaStream_t stream) {
 
 cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream) {
   if (a.nseg < 3) return cudaSuccess;  // slot 1 is the end state of segment 0 already
-  const int64_t n4 = a.b * a.H * ((int64_t)a.KD * a.VD / 4), grid = (n4 + 255) / 256;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  la_prefix_kernel<<<(unsigned)grid, 256, 0, stream>>>(a, n4, tc);
+  const int per = a.KD * a.VD / 4;
+  la_prefix_kernel<<<dim3((unsigned)(a.b * a.H), (unsigned)((per + 127) / 128)), 128, 0, stream>>>(a, per, tc);
   return cudaGetLastError();
 }
 

@@ -41,27 +41,30 @@ struct LaCore {
   int* status;
 };
 
+// Token indices fit 32 bits (L is at most 2^31 - 256); 64-bit divisions, repeated 64-bit exponentials and
+// unrolled set-up code are kept out of the kernels' prologues, where an instruction is fetched for one use.
 // Tokens of batch row bi that are read.
-__device__ __forceinline__ int64_t la_len(const LaCore& a, int bi) {
-  if (!a.lens) return a.L;
-  const int64_t n = a.lens[bi];
-  return n < 0 ? 0 : n > a.L ? a.L : n;
+__device__ __forceinline__ int la_len(const LaCore& a, int bi) {
+  const int L = (int)a.L;
+  if (!a.lens) return L;
+  const int n = a.lens[bi];
+  return n < 0 ? 0 : n > L ? L : n;
 }
 // g^e for a whole exponent e >= 0, rounded once to fp32: computed in 64 bits, so that distant tokens keep
 // their weight to fp32 accuracy.  g = 0 (log_decay = -inf) keeps g^0 = 1.
-__device__ __forceinline__ double la_pow(float log_decay, int64_t e) {
+static __device__ __noinline__ double la_pow(float log_decay, int e) {
   return e <= 0 ? 1.0 : exp((double)log_decay * (double)e);
 }
 // Tokens of segment m: [lo, hi) of the padded sequence, and how many of them are valid.
 struct SegSpan {
-  int64_t lo, hi, ta, tb;
+  int lo, hi, ta, tb;
 };
-__device__ __forceinline__ SegSpan la_span(const LaCore& a, int m, int64_t len) {
+__device__ __forceinline__ SegSpan la_span(const LaCore& a, int m, int len) {
   SegSpan s;
-  const int64_t p0 = (int64_t)m * a.seg_tok, p1 = p0 + a.seg_tok < a.L ? p0 + a.seg_tok : a.L;
-  s.lo = a.rev ? a.L - p1 : p0;
-  s.hi = a.rev ? a.L - p0 : p1;
-  if (s.hi < s.lo) s.hi = s.lo;
+  const unsigned L = (unsigned)a.L, seg = (unsigned)a.seg_tok;
+  const unsigned q0 = (unsigned)m * seg, p0 = q0 < L ? q0 : L, p1 = L - p0 > seg ? p0 + seg : L;
+  s.lo = (int)(a.rev ? L - p1 : p0);
+  s.hi = (int)(a.rev ? L - p0 : p1);
   s.ta = s.lo < len ? s.lo : len;
   s.tb = s.hi < len ? s.hi : len;
   return s;
@@ -70,20 +73,20 @@ constexpr int kLaChunk = 128;  // tokens of a chunk of the tensor-core form
 // The valid chunks of a segment, in processing order: chunk(i), i < n; chunks [z0, z1) of it lie
 // past the sequence's length.  A segment's tokens: those that are valid.
 struct ChunkSpan {
-  int64_t first, z0, z1, tokens;
-  int n;
+  int first, z0, z1, tokens, n;
 };
-__device__ __forceinline__ ChunkSpan la_chunks(const LaCore& a, int seg, int64_t len) {
-  const int64_t nch = (a.L + kLaChunk - 1) / kLaChunk, segc = a.seg_tok / kLaChunk, nvc = (len + kLaChunk - 1) / kLaChunk;
-  const int64_t p0 = seg * segc < nch ? seg * segc : nch, p1 = p0 + segc < nch ? p0 + segc : nch;
+__device__ __forceinline__ ChunkSpan la_chunks(const LaCore& a, int seg, int len) {
+  const int nch = ((int)a.L + kLaChunk - 1) / kLaChunk, segc = (int)a.seg_tok / kLaChunk;
+  const int nvc = (len + kLaChunk - 1) / kLaChunk;
+  const int p0 = seg * segc < nch ? seg * segc : nch, p1 = p0 + segc < nch ? p0 + segc : nch;
   ChunkSpan c;
-  const int64_t lo = a.rev ? nch - p1 : p0, hi = a.rev ? nch - p0 : p1;  // chunks [lo, hi)
-  const int64_t top = hi < nvc ? hi : nvc;
-  c.n = top > lo ? (int)(top - lo) : 0;
+  const int lo = a.rev ? nch - p1 : p0, hi = a.rev ? nch - p0 : p1;  // chunks [lo, hi)
+  const int top = hi < nvc ? hi : nvc;
+  c.n = top > lo ? top - lo : 0;
   c.first = a.rev ? top - 1 : lo;
   c.z0 = top > lo ? top : lo;
   c.z1 = hi;
-  const int64_t end = top * kLaChunk < len ? top * kLaChunk : len;
+  const int end = top * kLaChunk < len ? top * kLaChunk : len;
   c.tokens = c.n > 0 ? end - lo * kLaChunk : 0;
   return c;
 }

@@ -55,7 +55,7 @@ constexpr int LSC = LV / 2;    // value columns of a warp of either group
 constexpr uint32_t LN_SC = 1, LN_Y = 2, LN_H = 3, LN_YI = 4, LN_THREADS = 32 * (L_GROUP + 1);
 constexpr unsigned long long L_WAIT_NS = 2000000000ull;  // 2 s bound on any wait
 constexpr int LBLK = 128 * 128;                          // one 64-column block of a 128-row tile, bytes
-constexpr int L_MAXPOW = LQ + 1;
+constexpr int L_MAXPOW = LQ + 1;  // and one word for the rest of a^128
 
 // Barriers (pairs: one per stage).  None can complete two phases past a waiter (a parity wait would then
 // miss one): each phase needs what the waiter does after it has seen the one before, of the same pair entry.
@@ -86,7 +86,7 @@ struct LaCfg {
   static constexpr int OFF_VT = 2 * STAGE;         // three parts of the weighted v
   static constexpr int OFF_S = OFF_VT + 3 * LBLK;  // bf16(S), KD rows of 64
   static constexpr int OFF_POW = OFF_S + KD * 128;
-  static constexpr int OFF_COL = OFF_POW + ((L_MAXPOW * 4 + 15) & ~15);  // column factors of a 32-column score block
+  static constexpr int OFF_COL = OFF_POW + (((L_MAXPOW + 1) * 4 + 15) & ~15);  // column factors of a 32-column score block
   static constexpr int OFF_DIAG = OFF_COL + 32 * 4;                       // scaled weights of the diagonal blocks
   static constexpr int OFF_BAR = OFF_DIAG + 64 * 4;
   static constexpr int OFF_MISC = OFF_BAR + LNBAR * 8;
@@ -199,13 +199,12 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
   const int vtiles = a.VD / LV;
-  int64_t blk = blockIdx.x;
-  const int vt = (int)(blk % vtiles);
-  blk /= vtiles;
-  const int nseg_grid = FULL ? a.nseg : a.nseg - 1;
-  const int seg = (int)(blk % nseg_grid);
-  const int64_t bh = blk / nseg_grid;
-  const int bi = (int)(bh / a.H), h = (int)(bh % a.H);
+  unsigned blk = blockIdx.x;
+  const int vt = vtiles == 2 ? (int)(blk & 1) : 0;
+  if (vtiles == 2) blk >>= 1;
+  const unsigned nseg_grid = FULL ? a.nseg : a.nseg - 1;
+  const int seg = (int)(blk % nseg_grid), bh = (int)(blk / nseg_grid);
+  const int bi = bh / a.H, h = bh % a.H;
 
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
@@ -238,15 +237,17 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   float* colf = reinterpret_cast<float*>(sm + C::OFF_COL);
   float* diag = reinterpret_cast<float*>(sm + C::OFF_DIAG);
   if (tid < L_MAXPOW) {
-    const float w = (float)la_pow(ld, tid);
+    const double wd = la_pow(ld, tid);
+    const float w = (float)wd;
     pw[tid] = w;
+    if (tid == LQ) pw[LQ + 1] = (float)(wd - (double)w);  // a^128 as two floats
     if (tid < 32) {
       colf[a.rev ? tid : 31 - tid] = w;
       diag[31 + tid] = diag[31 - tid] = a.s_upd * a.s_out * w;  // weight of the distance |j - 31|
     }
   }
   const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
-  const int64_t len = page < 0 ? 0 : la_len(a, bi);
+  const int len = page < 0 ? 0 : la_len(a, bi);
   const ChunkSpan cs = la_chunks(a, seg, len);
   const int n = cs.n;
   tc_fence_before();
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
   auto chunk = [&](int i) { return a.rev ? cs.first - i : cs.first + i; };
   auto valid = [&](int i) {  // tokens of chunk i within the length
-    const int64_t left = len - chunk(i) * LQ;
-    return left < LQ ? (int)left : LQ;
+    const int left = len - chunk(i) * LQ;
+    return left < LQ ? left : LQ;
   };
 
   const int part = a.rev ? 0 : n - 1;  // the one chunk that the sequence's end may cut
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         // alone leave a load's latency, three thousand cycles from HBM, uncovered
         auto prefetch = [&](int i) {
           if (i >= n) return;
-          const int tok = (int)(chunk(i) * LQ);
+          const int tok = chunk(i) * LQ;
           tma_prefetch_4d(&tmV, LV * vt, gv, tok, bi);
           if (vt > 0) return;
 #pragma unroll
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         int done = 0;
         for (int i = 0; i < n; ++i) {
           prefetch(i + L_PREFETCH);
-          const int s = i & 1, tok = (int)(chunk(i) * LQ);
+          const int s = i & 1, tok = chunk(i) * LQ;
           const uint32_t before = (uint32_t)(((i >> 1) & 1) ^ 1);  // phase of the stage's chunk i - 2
           if (i >= 2 && !la_wait(B(LB_FK + s), before, abort_flag)) break;
           mbar_expect_tx(&bar[LB_LQK + s], FULL ? 2 * C::TILE_K : C::TILE_K);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
           ok = ok && la_wait(B(LB_YW + s), (uint32_t)((i >> 1) & 1), abort_flag);
           if (lane == 0 && ok) {
             if (!a.out_f32) {
-              tma_store_4d(&tmO, sQ(s), LV * vt, h, (int)(chunk(i) * LQ), bi);
+              tma_store_4d(&tmO, sQ(s), LV * vt, h, chunk(i) * LQ, bi);
               bulk_commit();
               bulk_wait_read();
             }
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         tc_fence_after();
         const bool on = t < nv;
         const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
-        const int64_t tok = chunk(i) * LQ + t;
+        const int tok = chunk(i) * LQ + t;
 #pragma unroll
         for (int c = 0; c < LSC / 16; ++c) {
           uint32_t x[16], y[16];
@@ -541,8 +542,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         arrive(LB_YW + s);
       }
       // chunks past the sequence's length
-      for (int64_t j = cs.z0; j < cs.z1; ++j) {
-        const int64_t tok = j * LQ + t;
+      for (int j = cs.z0; j < cs.z1; ++j) {
+        const int tok = j * LQ + t;
         if (tok >= a.L) continue;
         const int e = a.out_f32 ? 4 : 2;
         uint4* g = reinterpret_cast<uint4*>(static_cast<char*>(a.out) + out_row(tok) * e);
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     uint64_t S[LSC / 2];
 #pragma unroll
     for (int e = 0; e < LSC / 2; ++e) S[e] = 0;
-    auto slot = [&](int s) { return a.ws + ((bh * a.nseg + s) * KD + row) * (int64_t)a.VD + col; };
+    auto slot = [&](int s) { return a.ws + (((int64_t)bh * a.nseg + s) * KD + row) * a.VD + col; };
     const int64_t sbase = (page * a.H + h) * (int64_t)KD * a.VD + row * a.s_i + col * a.s_j;
     auto store_slot = [&](int s) {
       float4* p = reinterpret_cast<float4*>(slot(s));
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       const bool from_ws = FULL && a.nseg > 1;
       if (from_ws || (seg == 0 && a.s_in)) {
         const float* src = from_ws ? slot(seg) : a.s_in + sbase;
-        const int64_t sj = from_ws ? 1 : a.s_j;
+        const int sj = from_ws ? 1 : (int)a.s_j;
 #pragma unroll
         for (int e = 0; e < LSC / 2; ++e) S[e] = f2(src[2 * e * sj], src[(2 * e + 1) * sj]);
       }
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     };
 
     // the decay of a full chunk as two floats: a long memory multiplies it in hundreds of times
-    const float a128 = lds32(sPow + 4 * LQ), a128_lo = (float)(la_pow(ld, LQ) - (double)a128);
+    const float a128 = lds32(sPow + 4 * LQ), a128_lo = lds32(sPow + 4 * LQ + 4);
     if (n > 0) {
       if constexpr (FULL) publish();
       named_bar_sync(LN_H, LN_THREADS);
@@ -691,12 +692,14 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       if (!FULL) {
         store_slot(seg + 1);
       } else if (seg == a.nseg - 1 && a.s_fin) {
+        float* dst = a.s_fin + sbase;
+        const int sj = (int)a.s_j;
 #pragma unroll
         for (int e = 0; e < LSC / 2; ++e) {
           float lo, hi;
           f2_split(S[e], lo, hi);
-          a.s_fin[sbase + 2 * e * a.s_j] = lo;
-          a.s_fin[sbase + (2 * e + 1) * a.s_j] = hi;
+          dst[2 * e * sj] = lo;
+          dst[(2 * e + 1) * sj] = hi;
         }
       }
     }
