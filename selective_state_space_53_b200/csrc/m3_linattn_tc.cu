@@ -87,8 +87,7 @@ struct LaCfg {
   static constexpr int OFF_S = OFF_VT + 3 * LBLK;  // bf16(S), KD rows of 64
   static constexpr int OFF_POW = OFF_S + KD * 128;
   static constexpr int OFF_COL = OFF_POW + (((L_MAXPOW + 1) * 4 + 15) & ~15);  // column factors of a 32-column score block
-  static constexpr int OFF_DIAG = OFF_COL + 32 * 4;                       // scaled weights of the diagonal blocks
-  static constexpr int OFF_BAR = OFF_DIAG + 64 * 4;
+  static constexpr int OFF_BAR = OFF_COL + 32 * 4;
   static constexpr int OFF_MISC = OFF_BAR + LNBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
   static constexpr uint32_t TM_A = 0, TM_AP = 128, TM_YA = 192, TM_YI = 256, TM_H = 320, TM_COLS = 512;
@@ -197,7 +196,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   constexpr bool FULL = MODE == 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
+  // the warp index as a uniform value: addresses and branches that hang on it stay off the vector registers
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31, q4 = warp & 3;
   const int vtiles = a.VD / LV;
   unsigned blk = blockIdx.x;
   const int vt = vtiles == 2 ? (int)(blk & 1) : 0;
@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   }
   const float ld = a.log_decay[h];
   float* colf = reinterpret_cast<float*>(sm + C::OFF_COL);
-  float* diag = reinterpret_cast<float*>(sm + C::OFF_DIAG);
   if (tid < L_MAXPOW) {
     const double wd = la_pow(ld, tid);
     const float w = (float)wd;
@@ -243,7 +242,6 @@ __global__ void __launch_bounds__(L_THREADS, 1)
     if (tid == LQ) pw[LQ + 1] = (float)(wd - (double)w);  // a^128 as two floats
     if (tid < 32) {
       colf[a.rev ? tid : 31 - tid] = w;
-      diag[31 + tid] = diag[31 - tid] = a.s_upd * a.s_out * w;  // weight of the distance |j - 31|
     }
   }
   const int64_t page = la_page_block(a.pages, a.npages, bi, a.status);
@@ -253,7 +251,7 @@ __global__ void __launch_bounds__(L_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
   auto chunk = [&](int i) { return a.rev ? cs.first - i : cs.first + i; };
   auto valid = [&](int i) {  // tokens of chunk i within the length
@@ -443,59 +441,72 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       const int t = 32 * q4 + lane;        // this thread's token of a chunk
       const uint32_t ro = (uint32_t)t * 128u;
       const int64_t col = LV * vt + LSC * w;
-      // diagonal blocks: the weight of column e lies e words on (mirrored table), kept where bit e is set
-      const uint32_t sDg = sBase + C::OFF_DIAG + 4 * (31 - lane), sCol = sBase + C::OFF_COL;
-      const uint32_t keep = a.rev ? kFull << lane : kFull >> (31 - lane);
+      const uint32_t sCol = sBase + C::OFF_COL;
       const float sc = a.s_upd * a.s_out;
       auto out_row = [&](int64_t tok) { return (((int64_t)bi * a.L + tok) * a.H + h) * (int64_t)a.VD + col; };
+      // Blocks between the rows and a block of columns: below 0 it lies ahead and stays zero throughout.  The
+      // weights of one block are kept in registers: the diagonal one if the warp has it (zero where the column
+      // is ahead of the row), else its first; those of the other are made from a row and a column factor.
+      auto dist = [&](int cb) { return a.rev ? cb - q4 : q4 - cb; };
+      const bool swap = dist(w) != 0 && (dist(3 - w) == 0 || dist(w) < 0);
+      const int cb0 = swap ? 3 - w : w, cb1 = swap ? w : 3 - w, d0 = dist(cb0), d1 = dist(cb1);
+      uint64_t W[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int x0 = 32 * d0 + (a.rev ? 2 * e - lane : lane - 2 * e), x1 = x0 + (a.rev ? 1 : -1);
+        const float w0 = sc * lds32(sPow + 4 * (x0 < 0 ? 0 : x0)), w1 = sc * lds32(sPow + 4 * (x1 < 0 ? 0 : x1));
+        W[e] = f2(x0 < 0 ? 0.0f : w0, x1 < 0 ? 0.0f : w1);
+      }
+      {
+        uint32_t o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = 0u;
+        if (d0 < 0) tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb0, o);
+        if (d1 < 0) tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb1, o);
+      }
+      const float r1 = d1 > 0 ? sc * lds32(sPow + 4 * (a.rev ? 32 * d1 - lane : 32 * d1 - 31 + lane)) : 0.0f;
       for (int i = 0; i < n; ++i) {
         const int s = i & 1;
         const int nv = i == part ? nv_part : LQ;
         named_bar_sync(LN_SC, LN_THREADS);
         tc_fence_after();
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          const int cb = half ? 3 - w : w;           // block of columns
-          const int d = a.rev ? cb - q4 : q4 - cb;  // blocks between the rows and the columns
-          uint32_t o[16];
-          if (d < 0) {
+        auto finish = [&](int cb, uint32_t (&o)[16]) {
+          if (32 * cb + 32 > nv) {  // columns past the length
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          } else {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb, v);
-            if (d > 0) {
-              const float r = sc * lds32(sPow + 4 * (a.rev ? 32 * d - lane : 32 * d - 31 + lane));
-              const uint64_t r2 = f2(r, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint4 u = lds128(sCol + 16 * e);
-                float x0, x1, x2, x3;
-                f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
-                f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
-                o[2 * e] = pack_bf16(x0, x1);
-                o[2 * e + 1] = pack_bf16(x2, x3);
-              }
-            } else {
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                // a select: what lies ahead may be infinite
-                const float x0 = __uint_as_float(v[2 * e]) * lds32(sDg + 8 * e);
-                const float x1 = __uint_as_float(v[2 * e + 1]) * lds32(sDg + 8 * e + 4);
-                o[e] = pack_bf16((keep >> (2 * e)) & 1 ? x0 : 0.0f, (keep >> (2 * e + 1)) & 1 ? x1 : 0.0f);
-              }
-            }
-            if (32 * cb + 32 > nv) {  // columns past the length
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if (32 * cb + 2 * e >= nv) o[e] = 0u;
-                else if (32 * cb + 2 * e + 1 >= nv) o[e] &= 0xffffu;
-              }
+            for (int e = 0; e < 16; ++e) {
+              if (32 * cb + 2 * e >= nv) o[e] = 0u;
+              else if (32 * cb + 2 * e + 1 >= nv) o[e] &= 0xffffu;
             }
           }
           tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb, o);
+        };
+        if (d0 >= 0) {
+          uint32_t v[32], o[16];
+          tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            f2_split(f2_mul(f2_bits(v[2 * e], v[2 * e + 1]), W[e]), x0, x1);
+            o[e] = pack_bf16(x0, x1);
+          }
+          finish(cb0, o);
+        }
+        if (d1 >= 0) {
+          uint32_t v[32], o[16];
+          tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb1, v);
+          tmem_wait_ld();
+          const uint64_t r2 = f2(r1, r1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 u = lds128(sCol + 16 * e);
+            float x0, x1, x2, x3;
+            f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
+            f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
+            o[2 * e] = pack_bf16(x0, x1);
+            o[2 * e + 1] = pack_bf16(x2, x3);
+          }
+          finish(cb1, o);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -611,27 +622,24 @@ __global__ void __launch_bounds__(L_THREADS, 1)
       return t < nv ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
     };
     auto vchunk = [&](int c) { return ro + (uint32_t)(((c + 4 * w) ^ (t & 7)) << 4); };
-    auto finish = [&](int i) {  // the weighted v is complete
-      if (i == part && t >= nv_part) {  // no infinity or NaN found past the length meets a product
-        const int s = i & 1;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto weigh = [&](int i) {
+      if (i == part && nv_part < LQ) {  // no infinity or NaN found past the length meets a product
+        if (t >= nv_part) {
+          const int s = i & 1;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 4 * w; c < 4 * w + 4; ++c) {
-          sts128(sV(s) + ro + 16 * c, zero);
+          for (int c = 0; c < LSC / 8; ++c) {
+            sts128(sV(s) + vchunk(c), zero);
 #pragma unroll
-          for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + ro + 16 * c, zero);
+            for (int b = 0; b < KD / 64; ++b) sts128(sK(s) + b * LBLK + vchunk(c), zero);
+          }
         }
       }
-      fence_async_smem();
-      arrive(LB_VT);
-    };
-    auto weigh = [&](int i) {
       const float wt = weight(i);
       const uint64_t w2 = f2(wt, wt), minus = f2(-1.0f, -1.0f);
 #pragma unroll
       for (int c = 0; c < LSC / 8; ++c) {
-        uint4 raw = lds128(sV(i & 1) + vchunk(c));
-        if (i == part && t >= nv_part) raw = make_uint4(0, 0, 0, 0);  // past the length there may be anything
+        const uint4 raw = lds128(sV(i & 1) + vchunk(c));
         uint64_t f[4] = {f2_mul(f2(bf_lo(raw.x), bf_hi(raw.x)), w2), f2_mul(f2(bf_lo(raw.y), bf_hi(raw.y)), w2),
                          f2_mul(f2(bf_lo(raw.z), bf_hi(raw.z)), w2), f2_mul(f2(bf_lo(raw.w), bf_hi(raw.w)), w2)};
 #pragma unroll
@@ -649,7 +657,8 @@ __global__ void __launch_bounds__(L_THREADS, 1)
           sts128(sVT + q * LBLK + vchunk(c), make_uint4(b[0], b[1], b[2], b[3]));
         }
       }
-      finish(i);
+      fence_async_smem();
+      arrive(LB_VT);
     };
 
     // the decay of a full chunk as two floats: a long memory multiplies it in hundreds of times
