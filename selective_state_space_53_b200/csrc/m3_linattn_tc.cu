@@ -516,7 +516,6 @@ __global__ void __launch_bounds__(L_THREADS, 1)
         tc_fence_after();
         const bool on = t < nv;
         const float f = on ? a.s_out * lds32(sPow + 4 * (a.rev ? nv - 1 - t : t + 1)) : 0.0f;
-        const int tok = chunk(i) * LQ + t;
 #pragma unroll
         for (int c = 0; c < LSC / 16; ++c) {
           uint32_t x[16], y[16];
@@ -536,11 +535,23 @@ __global__ void __launch_bounds__(L_THREADS, 1)
             for (int e = 0; e < 16; ++e) v[e] = 0.0f;
           }
           if (a.out_f32) {
-            if (tok < a.L) {
-              float4* g = reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row(tok)) + 4 * c;
+            // the warp's 32 rows of 16 values over its 2 KB of q's tile (64-byte rows, 16-byte chunks rotated
+            // by the row), then four lanes to a row: full sectors, an eighth of the lines per store
+            const uint32_t sW = sQ(s) + 2048u * (warp - L_CTRL);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) g[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              sts128(sW + lane * 64 + (((e + (lane >> 1)) & 3) << 4),
+                     make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]),
+                                __float_as_uint(v[4 * e + 3])));
+            __syncwarp();
+            const int ch = lane & 3;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * e + (lane >> 2), rt = chunk(i) * LQ + 32 * q4 + r;
+              const uint4 x4 = lds128(sW + r * 64 + (((ch + (r >> 1)) & 3) << 4));
+              if (rt < a.L) reinterpret_cast<uint4*>(static_cast<float*>(a.out) + out_row(rt))[4 * c + ch] = x4;
             }
+            __syncwarp();
           } else {  // over q of the stage, which Yi was the last to read
 #pragma unroll
             for (int e = 0; e < 2; ++e)
