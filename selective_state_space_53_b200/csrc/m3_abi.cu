@@ -199,7 +199,9 @@ m3::LaCore la_forward(const m3_dims* d) {
 
 struct LaBwd {
   m3::LaCore dq, dk, dv;
-  size_t core, part;  // scratch: the largest of the passes', and the heads' shares of dq or dk (G < H)
+  bool joint;         // the three passes run as one launch
+  size_t core, part;  // scratch: the passes' own, and the heads' shares of dq or dk (G < H; two of them when joint)
+  size_t bytes() const { return core + (joint ? 2 : 1) * part; }
 };
 
 LaBwd la_backward(const m3_dims* d) {
@@ -217,13 +219,15 @@ LaBwd la_backward(const m3_dims* d) {
   if (d->G < d->H) w.dq.out_f32 = 1;
   w.dk = w.dq;
   w.dk.rev = 1;
-  w.core = 0;
-  for (const m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
-    const size_t n = m3::la_core_ws_bytes(*a);
-    if (n > w.core) w.core = n;
-  }
+  w.joint = m3::la_joint(w.dq, w.dk, w.dv);
+  w.core = w.joint ? 3 * m3::la_joint_ws_bytes(w.dv) : 0;
+  if (!w.joint)
+    for (const m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
+      const size_t n = m3::la_core_ws_bytes(*a);
+      if (n > w.core) w.core = n;
+    }
   w.core = (w.core + 255) & ~(size_t)255;
-  w.part = d->G < d->H ? sizeof(float) * (size_t)(d->b * d->L) * d->H * d->N : 0;
+  w.part = d->G < d->H ? (sizeof(float) * (size_t)(d->b * d->L) * d->H * d->N + 255) & ~(size_t)255 : 0;
   return w;
 }
 
@@ -659,7 +663,7 @@ m3_status m3_linattn_bwd_workspace_size(const m3_dims* dims, size_t* out_bytes) 
   if (st != M3_OK) return st;
   if (!out_bytes) return M3_ERR_NULL;
   const LaBwd w = la_backward(dims);
-  *out_bytes = w.core + w.part;
+  *out_bytes = w.bytes();
   return M3_OK;
 }
 
@@ -676,12 +680,13 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
     if (t && !aligned16(t)) return M3_ERR_ALIGN;
   if (!aligned4(log_decay) || !aligned4(lens)) return M3_ERR_ALIGN;
   LaBwd w = la_backward(dims);
-  const size_t need = w.core + w.part;
+  const size_t need = w.bytes();
   if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return M3_ERR_ALIGN;
   int* status = status_word();
   if (!status) return M3_ERR_CUDA;
   void* part = static_cast<char*>(workspace) + w.core;
+  void* part2 = w.joint ? static_cast<char*>(part) + w.part : part;
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t NP_rows = dims->b * dims->L;
   for (m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
@@ -702,7 +707,7 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
   w.dk.v = q;
   w.dk.s_upd = scale;
   w.dk.s_in = dstate_out;
-  w.dk.out = w.part ? part : dk;
+  w.dk.out = w.part ? part2 : dk;
   // dv = E^T k: (k, q, dy) against time
   w.dv.q = k;
   w.dv.k = q;
@@ -712,13 +717,22 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
   w.dv.s_fin = dstate_in;
   w.dv.out = dv;
   cudaError_t e = cudaSuccess;
+  auto sum = [&](const m3::LaCore& a, void* out) {  // the heads' shares of a group, in head order
+    return w.part ? m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, a.bf16, static_cast<float*>(a.out), out, s)
+                  : cudaSuccess;
+  };
+  if (w.joint) {
+    m3::LaCore cores[3] = {w.dq, w.dk, w.dv};
+    e = m3::launch_la_joint(cores, workspace, s);
+    if (e == cudaSuccess) e = sum(w.dq, dq);
+    if (e == cudaSuccess) e = sum(w.dk, dk);
+    return cuda_status(e);
+  }
   if (dims->L > 0) {
     e = m3::launch_la_core(w.dq, workspace, w.core, s);
-    if (e == cudaSuccess && w.part)
-      e = m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, w.dq.bf16, static_cast<float*>(part), dq, s);
+    if (e == cudaSuccess) e = sum(w.dq, dq);
     if (e == cudaSuccess) e = m3::launch_la_core(w.dk, workspace, w.core, s);
-    if (e == cudaSuccess && w.part)
-      e = m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, w.dk.bf16, static_cast<float*>(part), dk, s);
+    if (e == cudaSuccess) e = sum(w.dk, dk);
   }
   if (e == cudaSuccess) e = m3::launch_la_core(w.dv, workspace, w.core, s);
   return cuda_status(e);

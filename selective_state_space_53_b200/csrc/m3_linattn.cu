@@ -474,7 +474,7 @@ int cols_of(const LaCore& a) { return warps_of(a) * (128 / lanes_of(a.KD)); }
 // Segments of a sequence: enough for 16 warps per SM (about what the registers allow), each at
 // least 32 tokens long so that the walk outweighs reading the earlier segments' states.
 void plan_core(LaCore* a) {
-  if (la_tc_supported(*a)) return la_tc_plan(a, sm_count());
+  if (la_tc_supported(*a)) return la_tc_plan(a, sm_count(), 1);
   const int cols = cols_of(*a);
   const int64_t warps = a->b * a->H * ((a->VD + cols - 1) / cols) * warps_of(*a);
   int64_t nseg = warps > 0 ? (int64_t)sm_count() * 16 / warps : 1;
@@ -553,9 +553,29 @@ cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t str
   plan_core(&a);
   if (la_core_ws_bytes(a) > ws_bytes) return cudaErrorInvalidValue;
   a.ws = static_cast<float*>(ws);
-  if (la_tc_supported(a)) return launch_la_tc(a, stream);
+  if (la_tc_supported(a)) return launch_la_tc(&a, 1, stream);
   if (!a.bf16) return launch_core_type<false, true>(a, stream);
   return a.out_f32 ? launch_core_type<true, true>(a, stream) : launch_core_type<true, false>(a, stream);
+}
+
+bool la_joint(const LaCore& a, const LaCore& b, const LaCore& c) {
+  return la_tc_supported(a) && la_tc_supported(b) && la_tc_supported(c) && a.KD == b.KD && a.KD == c.KD &&
+         a.VD == b.VD && a.VD == c.VD;
+}
+
+size_t la_joint_ws_bytes(const LaCore& a0) {
+  LaCore a = a0;
+  la_tc_plan(&a, sm_count(), 3);
+  return a.nseg > 1 ? sizeof(float) * (size_t)(a.b * a.H) * a.nseg * a.KD * a.VD : 0;
+}
+
+cudaError_t launch_la_joint(LaCore* cores, void* ws, cudaStream_t stream) {
+  const size_t each = la_joint_ws_bytes(cores[0]) / sizeof(float);
+  for (int i = 0; i < 3; ++i) {
+    la_tc_plan(&cores[i], sm_count(), 3);
+    cores[i].ws = static_cast<float*>(ws) + i * each;
+  }
+  return launch_la_tc(cores, 3, stream);
 }
 
 cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,

@@ -110,8 +110,13 @@ __device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t n
 cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream);  // entering states from end states
 size_t la_core_ws_bytes(const LaCore& a);  // scratch of the pass (plans its segments)
 bool la_tc_supported(const LaCore& a);     // the tensor-core form takes this pass
-void la_tc_plan(LaCore* a, int sms);
-cudaError_t launch_la_tc(const LaCore& a, cudaStream_t stream);  // planned, scratch in a.ws
+void la_tc_plan(LaCore* a, int sms, int passes);
+// Up to three passes of the same sizes, planned alike, scratch in ws.
+cudaError_t launch_la_tc(const LaCore* cores, int n, cudaStream_t stream);
+// The gradients' passes may run as one launch (all on the tensor cores, N = P): then the scratch of each.
+bool la_joint(const LaCore& a, const LaCore& b, const LaCore& c);
+size_t la_joint_ws_bytes(const LaCore& a);
+cudaError_t launch_la_joint(LaCore* cores, void* ws, cudaStream_t stream);
 cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream);
 cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
                                cudaStream_t stream);

@@ -187,11 +187,23 @@ __device__ __forceinline__ void la_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Up to three passes in one launch (blockIdx.y): the gradients of one layer, whose CTAs then fill the
+// machine together.
+struct LaPass {
+  CUtensorMap q, k, v, o;
+  LaCore a;
+};
+struct LaJob {
+  LaPass p[3];
+};
+
 template <int KD, int MODE>
-__global__ void __launch_bounds__(L_THREADS, 1)
-    la_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                 const __grid_constant__ LaCore a) {
+__global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_constant__ LaJob job) {
+  const CUtensorMap& tmQ = job.p[blockIdx.y].q;
+  const CUtensorMap& tmK = job.p[blockIdx.y].k;
+  const CUtensorMap& tmV = job.p[blockIdx.y].v;
+  const CUtensorMap& tmO = job.p[blockIdx.y].o;
+  const LaCore& a = job.p[blockIdx.y].a;
   using C = LaCfg<KD>;
   constexpr bool FULL = MODE == 0;
   extern __shared__ uint8_t smem_raw[];
@@ -762,31 +774,35 @@ bool la_map(CUtensorMap* m, const LaCore& a, const void* base, int heads, int D)
 }
 
 template <int KD, int MODE>
-cudaError_t launch_tc_mode(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& o,
-                           const LaCore& a, cudaStream_t stream) {
+cudaError_t launch_tc_mode(const LaJob& job, int n, cudaStream_t stream) {
   static SmemAttr attr;
   auto kern = la_tc_kernel<KD, MODE>;
   const cudaError_t e = attr.ensure(kern, LaCfg<KD>::SMEM);
   if (e != cudaSuccess) return e;
+  const LaCore& a = job.p[0].a;
   const int64_t grid = a.b * a.H * (a.VD / LV) * (MODE == 0 ? a.nseg : a.nseg - 1);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned)grid, L_THREADS, LaCfg<KD>::SMEM, stream>>>(q, k, v, o, a);
+  kern<<<dim3((unsigned)grid, (unsigned)n), L_THREADS, LaCfg<KD>::SMEM, stream>>>(job);
   return cudaGetLastError();
 }
 
 template <int KD>
-cudaError_t launch_tc_kd(const LaCore& a, cudaStream_t stream) {
-  CUtensorMap q, k, v, o;
-  if (!la_map(&q, a, a.q, a.hq, KD) || !la_map(&k, a, a.k, a.hk, KD) || !la_map(&v, a, a.v, a.hv, a.VD))
-    return cudaErrorInvalidValue;
-  if (a.out_f32) o = v;  // unused: fp32 outputs are written from registers
-  else if (!la_map(&o, a, a.out, a.H, a.VD)) return cudaErrorInvalidValue;
-  if (a.nseg > 1) {
-    cudaError_t e = launch_tc_mode<KD, 1>(q, k, v, o, a, stream);
-    if (e == cudaSuccess) e = launch_la_prefix(a, true, stream);
+cudaError_t launch_tc_kd(const LaCore* cores, int n, cudaStream_t stream) {
+  LaJob job;
+  for (int i = 0; i < n; ++i) {
+    LaPass& p = job.p[i];
+    const LaCore& a = p.a = cores[i];
+    if (!la_map(&p.q, a, a.q, a.hq, KD) || !la_map(&p.k, a, a.k, a.hk, KD) || !la_map(&p.v, a, a.v, a.hv, a.VD))
+      return cudaErrorInvalidValue;
+    if (a.out_f32) p.o = p.v;  // unused: fp32 outputs are written from registers
+    else if (!la_map(&p.o, a, a.out, a.H, a.VD)) return cudaErrorInvalidValue;
+  }
+  if (cores[0].nseg > 1) {
+    cudaError_t e = launch_tc_mode<KD, 1>(job, n, stream);
+    for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_la_prefix(cores[i], true, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_tc_mode<KD, 0>(q, k, v, o, a, stream);
+  return launch_tc_mode<KD, 0>(job, n, stream);
 }
 
 }  // namespace
@@ -798,8 +814,8 @@ bool la_tc_supported(const LaCore& a) {
 // Segments of a sequence: the count with the least modelled time, in units of one chunk of the full
 // pass: waves of CTAs times chunks each, a state-pass chunk at half a unit, and four units for the
 // second launch.
-void la_tc_plan(LaCore* a, int sms) {
-  const int64_t nch = (a->L + LQ - 1) / LQ, units = a->b * a->H * (a->VD / LV);
+void la_tc_plan(LaCore* a, int sms, int passes) {
+  const int64_t nch = (a->L + LQ - 1) / LQ, units = a->b * a->H * (a->VD / LV) * passes;
   const int64_t most = nch < 32 ? nch : 32;
   double best = 0.0;
   int64_t segc = nch;
@@ -816,8 +832,8 @@ void la_tc_plan(LaCore* a, int sms) {
   a->nseg = (int)((nch + segc - 1) / segc);
 }
 
-cudaError_t launch_la_tc(const LaCore& a, cudaStream_t stream) {
-  return a.KD == 64 ? launch_tc_kd<64>(a, stream) : launch_tc_kd<128>(a, stream);
+cudaError_t launch_la_tc(const LaCore* cores, int n, cudaStream_t stream) {
+  return cores[0].KD == 64 ? launch_tc_kd<64>(cores, n, stream) : launch_tc_kd<128>(cores, n, stream);
 }
 
 }  // namespace m3
