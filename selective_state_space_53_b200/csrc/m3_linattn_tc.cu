@@ -48,7 +48,7 @@ constexpr int LV = 64;   // value columns of a CTA
 constexpr int L_PROD = 0, L_MMA = 1, L_STORE = 2, L_SIGNAL = 3;  // L_STORE also signals the score group
 constexpr int L_CTRL = 4;       // control warps
 constexpr int L_THREADS = 640;
-constexpr int L_PREFETCH = 4;  // chunks that L2 is asked for ahead of their loads
+constexpr int L_PREFETCH = 3;  // chunks that L2 is asked for ahead of their loads
 constexpr int L_GROUP = 8;     // warps of the score group and of the state group
 constexpr int LSC = LV / 2;    // value columns of a warp of either group
 // named barriers of a signal warp and its group: what the group waits for
