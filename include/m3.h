@@ -308,11 +308,13 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  *     its outputs are zero and no state is touched.  So does a page past the pool, and a page that
  *     an earlier row of the batch holds already; both also leave M3_ERR_STATE for m3_check.
  * lens and pages need 4-byte alignment only.  Outputs must not overlap inputs.
- * Precision: fp32 throughout for fp32 tensors, for sizes outside the tensor-core tiles and in the
- * step.  With bf16 tensors and N, P in {64, 128} the products of m3_linattn_fwd and m3_linattn_bwd
- * run on the tensor cores with fp32 accumulation: the weighted scores and the copy of the state
- * that q meets are rounded to bf16; the state itself stays fp32 (its updates enter as three bf16
- * parts, 24 bits).
+ * Precision: fp32 throughout for fp32 tensors, for sizes outside the tensor-core tiles, for the
+ * shortest sequences and in the step.  With bf16 tensors, N, P in {64, 128} and more than 24 tokens
+ * (gradients: 12) the products run on the tensor cores with fp32 accumulation, in chunks of 128
+ * tokens: the weighted scores and the copy of the state that q meets are rounded to bf16; the state
+ * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  There an infinity or NaN in a
+ * token may also reach the other tokens of its chunk, earlier ones included (a masked score is zero,
+ * and zero times infinity is not); tokens past a sequence's length never matter.
  */
 
 /* Scratch bytes m3_linattn_fwd needs for these dims (0 when it needs none). */

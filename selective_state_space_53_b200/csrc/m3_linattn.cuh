@@ -33,6 +33,7 @@ struct LaCore {
   const float* s_in;       // state row + head * KD * VD + i * s_i + j * s_j (key index i, value index j); may be null
   float* s_fin;            // the same layout; may be null, may be s_in
   int64_t s_i, s_j;
+  int tc_from;             // the fewest tokens that the tensor-core form takes (its chunk costs the same for one as for 128)
   int nseg;                // segments of a sequence walked in parallel
   int64_t seg_tok;         // tokens of a segment (in processing order)
   float* ws;               // (b * H, nseg, KD, VD) when nseg > 1: slot 0 the incoming state, slot m + 1

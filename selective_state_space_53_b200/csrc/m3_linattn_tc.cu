@@ -808,7 +808,7 @@ cudaError_t launch_tc_kd(const LaCore* cores, int n, cudaStream_t stream) {
 }  // namespace
 
 bool la_tc_supported(const LaCore& a) {
-  return a.bf16 && a.L > 0 && (a.KD == 64 || a.KD == 128) && (a.VD == 64 || a.VD == 128);
+  return a.bf16 && a.L >= a.tc_from && (a.KD == 64 || a.KD == 128) && (a.VD == 64 || a.VD == 128);
 }
 
 // Segments of a sequence: the count with the least modelled time, in units of one chunk of the full

@@ -64,20 +64,24 @@ def spoil(dev, lens):
             dev[name][i, n:, ..., ::3] = float("inf")
 
 
-def on_tiles(N, P, dtype):
-    return dtype == "bf16" and N in (64, 128) and P in (64, 128)
+def on_tiles(N, P, dtype, L=128, least=25):
+    return dtype == "bf16" and N in (64, 128) and P in (64, 128) and L >= least
 
 
 # b, L, H, G, N, P, dtype, lens, state, decay
 SHAPES = [
     (1, 1, 1, 1, 64, 64, "bf16", None, False, None),
     (2, 1, 3, 1, 128, 128, "bf16", None, True, None),
+    (3, 25, 2, 1, 128, 128, "bf16", [25, 1, 13], True, None),
+    (2, 13, 4, 1, 64, 64, "bf16", [13, 7], True, None),
     (2, 127, 2, 2, 64, 64, "bf16", None, True, None),
     (1, 128, 4, 2, 128, 64, "bf16", None, False, None),
     (3, 129, 2, 1, 64, 128, "bf16", [129, 0, 128], True, None),
     (2, 300, 4, 4, 128, 128, "bf16", [1, 300], True, None),
     (1, 1500, 2, 1, 128, 128, "bf16", None, True, None),
     (2, 1111, 1, 1, 64, 64, "bf16", [700, 257], True, None),
+    (1, 2000, 3, 1, 64, 128, "bf16", [1921], True, None),
+    (3, 640, 6, 2, 64, 64, "bf16", [640, 513, 30], True, None),
     (1, 700, 5, 1, 128, 128, "bf16", None, True, [0.0, -1e-4, -3.0, -60.0, -np.inf]),
     (1, 400, 3, 3, 64, 128, "bf16", [383], True, [0.0, -40.0, -np.inf]),
     (2, 37, 2, 1, 8, 8, "f32", None, True, None),
@@ -106,7 +110,7 @@ def test_forward(b, L, H, G, N, P, dtype, lens, state, decay):
     torch.cuda.synchronize()
     assert m3.m3_check() == 0
     c = 2 * (2 * L + N + P) + 512
-    check("y", y, y_ref, y_mag, c, dtype, on_tiles(N, P, dtype))
+    check("y", y, y_ref, y_mag, c, dtype, on_tiles(N, P, dtype, L))
     check("state", s, s_ref, s_mag, c)
 
 
@@ -127,7 +131,7 @@ def test_backward(b, L, H, G, N, P, dtype, lens, state, decay):
     torch.cuda.synchronize()
     assert m3.m3_check() == 0
     c = 2 * (2 * L + N + P) + 512 + H // G
-    tiles = on_tiles(N, P, dtype)
+    tiles = on_tiles(N, P, dtype, L, 13)
     check("dq", g["dq"], ref[0], mag[0], c, dtype, tiles)
     check("dk", g["dk"], ref[1], mag[1], c, dtype, tiles)
     check("dv", g["dv"], ref[2], mag[2], c, dtype, tiles)
@@ -202,7 +206,8 @@ def test_pages_that_cannot_be_used(call):
     b, H, rows = 5, 2, 6
     N = P = 64 if call == "fwd_tiles" else 16
     dtype = "bf16" if call == "fwd_tiles" else "f32"
-    dev, host = draw(b, 9, H, H, N, P, dtype, seed=5)
+    L = 40 if call == "fwd_tiles" else 9  # past the shortest sequences: the tensor-core form
+    dev, host = draw(b, L, H, H, N, P, dtype, seed=5)
     pages = np.array([2, 4, 2, 6, -3], np.int32)
     pool = np.random.default_rng(6).standard_normal((rows, H, N, P)).astype(np.float32)
     tp = torch.from_numpy(pool).cuda()
@@ -217,7 +222,7 @@ def test_pages_that_cannot_be_used(call):
     args = [host[n][:2] for n in "qkv"]
     y_ref, s_ref = ola.forward(*args, host["ld"], N ** -0.5, state=pool[pages[:2]])
     y_mag, s_mag = ola.forward(*(np.abs(a) for a in args), host["ld"], N ** -0.5, state=np.abs(pool[pages[:2]]))
-    c = 2 * (18 + N + P) + 512
+    c = 2 * (2 * L + N + P) + 512
     check("y", y[:2], y_ref, y_mag, c, dtype, call == "fwd_tiles")
     assert not y[2:].any()
     check("state", tp[[2, 4]], s_ref, s_mag, c)
@@ -289,3 +294,46 @@ def test_streams_and_captured_graphs():
         assert torch.equal(fy[0], wy[0]) and torch.equal(fy[1], wy[1])
         assert all(torch.equal(fb[n], wb[n]) for n in wb)
     assert m3.m3_check() == 0
+
+
+@pytest.mark.parametrize("N,P,dtype", [(64, 64, "bf16"), (24, 40, "f32")])
+def test_gradients_equal_differences(N, P, dtype):
+    """The gradients against central differences of the GPU's own forward loss in a random direction, summed
+    in 64 bits.  The loss is linear in v and in the state: their differences carry the rounding of y alone
+    (2^-8 or 2^-24 a step, independent over the outputs), compared against eight times its random-walk size."""
+    b, L, H, G = 2, 150, 2, 1
+    dev, _ = draw(b, L, H, G, N, P, dtype, seed=11)
+    ds = dev["ds"].double()
+
+    def loss(v, s0):
+        y, s = m3.linattn(dev["q"], dev["k"], v, dev["ld"], state=s0.clone())
+        return (dev["dy"].double() * y.double()).sum() + (ds * s.double()).sum(), y
+
+    g = m3.linattn_backward(dev["q"], dev["k"], dev["v"], dev["ld"], dev["dy"], state0=dev["s"], dstate=dev["ds"])
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -18  # of an output, operand roundings included
+    dv = torch.sign(g["dv"]).to(DT[dtype])
+    up, y = loss(dev["v"] + dv, dev["s"])
+    down, _ = loss(dev["v"] - dv, dev["s"])
+    step = ((dev["v"] + dv).double() - (dev["v"] - dv).double())  # as rounded
+    want = (g["dv"].double() * step).sum()
+    noise = 8 * half * float((dev["dy"].double() * y.double()).square().sum().sqrt()) * 2
+    gnoise = 8 * half * float((g["dv"].double() * step).square().sum().sqrt())
+    assert abs(float(up - down - want)) <= noise + gnoise
+    sdir = torch.sign(g["dstate0"])
+    up, y = loss(dev["v"], dev["s"] + sdir)
+    down, _ = loss(dev["v"], dev["s"] - sdir)
+    want = (g["dstate0"].double() * ((dev["s"] + sdir).double() - (dev["s"] - sdir).double())).sum()
+    noise = 8 * half * float((dev["dy"].double() * y.double()).square().sum().sqrt()) * 2
+    assert abs(float(up - down - want)) <= noise
+
+
+def test_tensors_on_another_stream_and_device_guard():
+    """A call inside a stream context runs there and allocates there."""
+    dev, _ = draw(1, 200, 2, 1, 64, 64, "bf16", seed=12)
+    want, _ = m3.linattn(dev["q"], dev["k"], dev["v"], dev["ld"])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        y, _ = m3.linattn(dev["q"], dev["k"], dev["v"], dev["ld"])
+    st.synchronize()
+    assert torch.equal(y, want)
