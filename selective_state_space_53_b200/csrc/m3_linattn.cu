@@ -6,8 +6,9 @@
 // state elements (k v, the decayed update, the readout) and the operand rows come from shared
 // memory as broadcast 128-bit loads.  LN = KD / 8 lanes share a column, their readouts are summed
 // by a shuffle reduce-scatter.  It is bound by the latency of a token's chain (loads, updates,
-// shuffles) at few warps and by the fp32 pipe, 6 KD VD flops a token and head, at many.  (16 rows a
-// thread took 168 registers: 97 us against FWDUS at b5 L1037 H6 N40 P56.)
+// shuffles) at few warps and by the fp32 pipe, 6 KD VD flops a token and head, at many.  At b5 L1037 H6
+// N40 P56 fp32 a call takes 56 us (its floor by bytes is 1.4 us), about 125 instructions a token and warp, half of
+// them the packed arithmetic; 16 rows a thread took 168 registers and 97 us.
 // Few sequences are cut into segments: every segment but the last is walked from a zero start (MODE 1)
 // and leaves its end state, a prefix pass turns the end states into entering states, and the full pass
 // starts from those.

@@ -34,6 +34,14 @@
 // MMA order per chunk i: update(i), Yi(i), Ya(i), A(i+1).  The scores of i run behind update and Yi, the
 // outputs behind A(i+1) and the next update; the weighted v of i + 1 (whose buffer the update of i has
 // read then) and the state behind Yi to A(i+1).
+// Why this split: q, k (32 KiB each at KD = 128), v and the three parts of the weighted v take 208 KiB at 64
+// value columns with two stages of q, k and v, so a head of 128 value columns is two CTAs, which repeat A and
+// its scores and share q and k in L2.
+// Measured: b2 L32768 H32 N = P = 128 with own q and k 0.54 ms, 4.0 TB/s of algorithmic traffic (61 % of the
+// measured copy rate); with shared q and k 0.50 ms.  Under a sustained load the board's power cap brings the
+// clock to 1.47 GHz and the call to 0.65 ms.  A chunk takes about 3900 cycles against 2500 of products and 2900
+// of shared-memory traffic: what bounds it is the latency of the SIMT tasks between the products (40 % of
+// the issue slots are used), not a pipe.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -353,8 +353,11 @@ def _la_rows(what, dims, state, pages, device):
     """Rows of the state pool a call works on, after the checks of state and pages."""
     import torch
     rows = dims.b if pages is None else state.shape[0]
-    _expect(what, "state", state, (rows, dims.H, dims.N, dims.P), torch.float32, device)
-    if pages is not None:
+    shape = (rows, dims.H, dims.N, dims.P)
+    if not (state.dtype is torch.float32 and state.shape == shape and state.device == device and state.is_contiguous()):
+        _expect(what, "state", state, shape, torch.float32, device)
+    if pages is not None and not (pages.dtype is torch.int32 and pages.shape == (dims.b,) and pages.device == device
+                                  and pages.is_contiguous()):
         _expect(what, "pages", pages, (dims.b,), torch.int32, device)
     return rows
 
@@ -511,10 +514,12 @@ class Pages:
 
     def _list(self, what, name, t):
         import torch
-        if t.dim() != 1:
-            raise M3Error(-1, f"{what}: {name} has shape {tuple(t.shape)}, expected one axis")
-        _expect(what, name, t, t.shape, torch.int32, self.device)
-        return t.shape[0]
+        shape = t.shape
+        if len(shape) != 1:
+            raise M3Error(-1, f"{what}: {name} has shape {tuple(shape)}, expected one axis")
+        if not (t.dtype is torch.int32 and t.device == self.device and t.is_contiguous()):
+            _expect(what, name, t, shape, torch.int32, self.device)
+        return shape[0]
 
     def copy(self, src, dst, stream=None):
         """Page dst[i] becomes a copy of page src[i], in list order (m3_pages_copy)."""
