@@ -202,9 +202,9 @@ m3::LaCore la_forward(const m3_dims* d) {
 
 struct LaBwd {
   m3::LaCore dq, dk, dv;
-  bool joint;         // the three passes run as one launch
-  size_t core, part;  // scratch: the passes' own, and the heads' shares of dq or dk (G < H; two of them when joint)
-  size_t bytes() const { return core + (joint ? 2 : 1) * part; }
+  int first;          // passes of the first group: dq and dk, and dv where it is alike
+  size_t core, part;  // scratch: the larger group's, and the heads' shares of dq and of dk each (G < H)
+  size_t bytes() const { return core + 2 * part; }
 };
 
 LaBwd la_backward(const m3_dims* d) {
@@ -223,13 +223,12 @@ LaBwd la_backward(const m3_dims* d) {
   if (d->G < d->H) w.dq.out_f32 = 1;
   w.dk = w.dq;
   w.dk.rev = 1;
-  w.joint = m3::la_joint(w.dq, w.dk, w.dv);
-  w.core = w.joint ? 3 * m3::la_joint_ws_bytes(w.dv) : 0;
-  if (!w.joint)
-    for (const m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
-      const size_t n = m3::la_core_ws_bytes(*a);
-      if (n > w.core) w.core = n;
-    }
+  w.first = m3::la_alike(w.dq, w.dv) ? 3 : 2;
+  w.core = m3::la_group_ws_bytes(w.dq, w.first);
+  if (w.first == 2) {
+    const size_t n = m3::la_group_ws_bytes(w.dv, 1);
+    if (n > w.core) w.core = n;
+  }
   w.core = (w.core + 255) & ~(size_t)255;
   w.part = d->G < d->H ? (sizeof(float) * (size_t)(d->b * d->L) * d->H * d->N + 255) & ~(size_t)255 : 0;
   return w;
@@ -593,7 +592,7 @@ m3_status m3_linattn_workspace_size(const m3_dims* dims, size_t* out_bytes) {
   m3_status st = check_la_dims(dims);
   if (st != M3_OK) return st;
   if (!out_bytes) return M3_ERR_NULL;
-  *out_bytes = m3::la_core_ws_bytes(la_forward(dims));
+  *out_bytes = m3::la_group_ws_bytes(la_forward(dims), 1);
   return M3_OK;
 }
 
@@ -610,7 +609,7 @@ m3_status m3_linattn_fwd(const m3_dims* dims, const void* q, const void* k, cons
     if (t && !aligned16(t)) return M3_ERR_ALIGN;
   if (!aligned4(log_decay) || !aligned4(lens) || !aligned4(pages)) return M3_ERR_ALIGN;
   m3::LaCore a = la_forward(dims);
-  const size_t need = m3::la_core_ws_bytes(a);
+  const size_t need = m3::la_group_ws_bytes(a, 1);
   if (need > 0 && (!workspace || workspace_bytes < need)) return M3_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return M3_ERR_ALIGN;
   a.q = q;
@@ -626,7 +625,9 @@ m3_status m3_linattn_fwd(const m3_dims* dims, const void* q, const void* k, cons
   a.s_fin = state_out;
   a.status = status_word();
   if (!a.status) return M3_ERR_CUDA;
-  return cuda_status(m3::launch_la_core(a, workspace, need, (cudaStream_t)stream));
+  m3::LaCores job{};
+  job.p[0] = a;
+  return cuda_status(m3::launch_la_group(&job, 1, workspace, need, (cudaStream_t)stream));
 }
 
 m3_status m3_linattn_step(const m3_dims* dims, const void* q_t, const void* k_t, const void* v_t,
@@ -690,7 +691,7 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
   int* status = status_word();
   if (!status) return M3_ERR_CUDA;
   void* part = static_cast<char*>(workspace) + w.core;
-  void* part2 = w.joint ? static_cast<char*>(part) + w.part : part;
+  void* part2 = static_cast<char*>(part) + w.part;
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t NP_rows = dims->b * dims->L;
   for (m3::LaCore* a : {&w.dq, &w.dk, &w.dv}) {
@@ -721,24 +722,20 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
   w.dv.s_fin = dstate_in;
   w.dv.out = dv;
   cudaError_t e = cudaSuccess;
-  auto sum = [&](const m3::LaCore& a, void* out) {  // the heads' shares of a group, in head order
-    return w.part ? m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, a.bf16, static_cast<float*>(a.out), out, s)
-                  : cudaSuccess;
-  };
-  if (w.joint) {
-    m3::LaCore cores[3] = {w.dq, w.dk, w.dv};
-    e = m3::launch_la_joint(cores, workspace, s);
-    if (e == cudaSuccess) e = sum(w.dq, dq);
-    if (e == cudaSuccess) e = sum(w.dk, dk);
-    return cuda_status(e);
-  }
   if (dims->L > 0) {
-    e = m3::launch_la_core(w.dq, workspace, w.core, s);
-    if (e == cudaSuccess) e = sum(w.dq, dq);
-    if (e == cudaSuccess) e = m3::launch_la_core(w.dk, workspace, w.core, s);
-    if (e == cudaSuccess) e = sum(w.dk, dk);
+    m3::LaCores job{{w.dq, w.dk, w.dv}};
+    e = m3::launch_la_group(&job, w.first, workspace, w.core, s);
+    if (e == cudaSuccess && w.part) {  // the heads' shares of a group, in head order
+      const float* parts[] = {static_cast<float*>(part), static_cast<float*>(part2)};
+      void* sums[] = {dq, dk};
+      e = m3::launch_la_head_sum(NP_rows, dims->H, dims->G, dims->N, w.dq.bf16, parts, sums, 2, s);
+    }
   }
-  if (e == cudaSuccess) e = m3::launch_la_core(w.dv, workspace, w.core, s);
+  if (e == cudaSuccess && (dims->L == 0 || w.first == 2)) {
+    m3::LaCores job{};
+    job.p[0] = w.dv;
+    e = m3::launch_la_group(&job, 1, workspace, w.core, s);
+  }
   return cuda_status(e);
 }
 

@@ -46,7 +46,8 @@ __device__ __forceinline__ float4 row4(const void* p, int i) {
 }
 
 template <bool BF16, bool OUT_F32, int LN, int MODE>
-__global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, int coltiles, int cols) {
+__global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_constant__ LaCores job, int coltiles, int cols) {
+  const LaCore& a = job.p[blockIdx.y];
   constexpr bool FULL = MODE == 0;
   constexpr int KDP = 8 * LN, CPW = 128 / LN, E = BF16 ? 2 : 4;
   using T = typename std::conditional<BF16, __nv_bfloat16, float>::type;
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const LaCore a, 
 // The states entering the segments: slot m + 1 holds the end state of segment m from a zero start (segment 0:
 // from slot 0) and becomes the state entering segment m + 1.  One thread per four state elements, the
 // segments in order; the loads do not wait for the sums.
-__global__ void __launch_bounds__(128) la_prefix_kernel(const LaCore a, int per, int tc) {
+__global__ void __launch_bounds__(128) la_prefix_kernel(const __grid_constant__ LaCores job, int per, int tc) {
+  const LaCore& a = job.p[blockIdx.z];
   const int bh = blockIdx.x, e4 = blockIdx.y * 128 + threadIdx.x;
   const int bi = bh / a.H, h = bh % a.H;
   __shared__ float f[kMaxSeg];  // the decay over each segment
@@ -347,7 +349,9 @@ __global__ void __launch_bounds__(128) la_prefix_kernel(const LaCore a, int per,
 
 // out (rows, G, D) = sum over the H / G heads of a group of part (rows, H, D), in head order.
 template <bool BF16>
-__global__ void __launch_bounds__(256) la_head_sum_kernel(int64_t n4, int H, int G, int D4, const float4* part, void* out) {
+__global__ void __launch_bounds__(256) la_head_sum_kernel(int64_t n4, int H, int G, int D4, const float4* part0, void* out0, const float4* part1, void* out1) {
+  const float4* part = blockIdx.y ? part1 : part0;
+  void* out = blockIdx.y ? out1 : out0;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   const int d = (int)(i % D4);
@@ -474,10 +478,10 @@ int cols_of(const LaCore& a) { return warps_of(a) * (128 / lanes_of(a.KD)); }
 
 // Segments of a sequence: enough for 16 warps per SM (about what the registers allow), each at
 // least 32 tokens long so that the walk outweighs reading the earlier segments' states.
-void plan_core(LaCore* a) {
-  if (la_tc_supported(*a)) return la_tc_plan(a, sm_count(), 1);
+void plan_core(LaCore* a, int passes) {
+  if (la_tc_supported(*a)) return la_tc_plan(a, sm_count(), passes);
   const int cols = cols_of(*a);
-  const int64_t warps = a->b * a->H * ((a->VD + cols - 1) / cols) * warps_of(*a);
+  const int64_t warps = a->b * a->H * ((a->VD + cols - 1) / cols) * warps_of(*a) * passes;
   int64_t nseg = warps > 0 ? (int64_t)sm_count() * 16 / warps : 1;
   const int64_t most = a->L / 32;
   if (nseg > most) nseg = most;
@@ -489,7 +493,8 @@ void plan_core(LaCore* a) {
 }
 
 template <bool BF16, bool OUT_F32, int LN, int MODE>
-cudaError_t launch_core_cfg(const LaCore& a, cudaStream_t stream) {
+cudaError_t launch_core_cfg(const LaCores& job, int n, cudaStream_t stream) {
+  const LaCore& a = job.p[0];
   const int cols = cols_of(a);
   const int bytes = 2 * kTB * (2 * 8 * LN + cols) * (BF16 ? 2 : 4) + kTB * cols * 4;
   static SmemAttr attr;
@@ -499,29 +504,29 @@ cudaError_t launch_core_cfg(const LaCore& a, cudaStream_t stream) {
   const int tiles = (a.VD + cols - 1) / cols;
   const int64_t grid = a.b * a.H * tiles * (MODE == 0 ? a.nseg : a.nseg - 1);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  k<<<(unsigned)grid, 32 * warps_of(a), bytes, stream>>>(a, tiles, cols);
+  k<<<dim3((unsigned)grid, (unsigned)n), 32 * warps_of(a), bytes, stream>>>(job, tiles, cols);
   return cudaGetLastError();
 }
 
 template <bool BF16, bool OUT_F32, int LN>
-cudaError_t launch_core_ln(const LaCore& a, cudaStream_t stream) {
-  if (a.nseg > 1) {
-    cudaError_t e = launch_core_cfg<BF16, BF16 ? false : true, LN, 1>(a, stream);
-    if (e == cudaSuccess) e = launch_la_prefix(a, false, stream);
+cudaError_t launch_core_ln(const LaCores& job, int n, cudaStream_t stream) {
+  if (job.p[0].nseg > 1) {
+    cudaError_t e = launch_core_cfg<BF16, BF16 ? false : true, LN, 1>(job, n, stream);
+    if (e == cudaSuccess) e = launch_la_prefix(job, n, false, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_core_cfg<BF16, OUT_F32, LN, 0>(a, stream);
+  return launch_core_cfg<BF16, OUT_F32, LN, 0>(job, n, stream);
 }
 
 template <bool BF16, bool OUT_F32>
-cudaError_t launch_core_type(const LaCore& a, cudaStream_t stream) {
-  switch (lanes_of(a.KD)) {
-    case 1: return launch_core_ln<BF16, OUT_F32, 1>(a, stream);
-    case 2: return launch_core_ln<BF16, OUT_F32, 2>(a, stream);
-    case 4: return launch_core_ln<BF16, OUT_F32, 4>(a, stream);
-    case 8: return launch_core_ln<BF16, OUT_F32, 8>(a, stream);
-    case 16: return launch_core_ln<BF16, OUT_F32, 16>(a, stream);
-    default: return launch_core_ln<BF16, OUT_F32, 32>(a, stream);
+cudaError_t launch_core_type(const LaCores& job, int n, cudaStream_t stream) {
+  switch (lanes_of(job.p[0].KD)) {
+    case 1: return launch_core_ln<BF16, OUT_F32, 1>(job, n, stream);
+    case 2: return launch_core_ln<BF16, OUT_F32, 2>(job, n, stream);
+    case 4: return launch_core_ln<BF16, OUT_F32, 4>(job, n, stream);
+    case 8: return launch_core_ln<BF16, OUT_F32, 8>(job, n, stream);
+    case 16: return launch_core_ln<BF16, OUT_F32, 16>(job, n, stream);
+    default: return launch_core_ln<BF16, OUT_F32, 32>(job, n, stream);
   }
 }
 
@@ -537,57 +542,54 @@ cudaError_t launch_step_cfg(const LaStep& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream) {
+cudaError_t launch_la_prefix(const LaCores& job, int n, bool tc, cudaStream_t stream) {
+  const LaCore& a = job.p[0];
   if (a.nseg < 3) return cudaSuccess;  // slot 1 is the end state of segment 0 already
   const int per = a.KD * a.VD / 4;
-  la_prefix_kernel<<<dim3((unsigned)(a.b * a.H), (unsigned)((per + 127) / 128)), 128, 0, stream>>>(a, per, tc);
+  la_prefix_kernel<<<dim3((unsigned)(a.b * a.H), (unsigned)((per + 127) / 128), (unsigned)n), 128, 0, stream>>>(job, per, tc);
   return cudaGetLastError();
 }
 
-size_t la_core_ws_bytes(const LaCore& a0) {
-  LaCore a = a0;
-  plan_core(&a);
+bool la_alike(const LaCore& a, const LaCore& b) {
+  const bool tc = la_tc_supported(a);
+  return tc == la_tc_supported(b) && a.KD == b.KD && a.VD == b.VD && (tc || a.out_f32 == b.out_f32);
+}
+
+namespace {
+size_t pass_ws_bytes(const LaCore& a) {  // of a planned pass
   return a.nseg > 1 ? sizeof(float) * (size_t)(a.b * a.H) * a.nseg * a.KD * a.VD : 0;
 }
+}  // namespace
 
-cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  plan_core(&a);
-  if (la_core_ws_bytes(a) > ws_bytes) return cudaErrorInvalidValue;
-  a.ws = static_cast<float*>(ws);
-  if (la_tc_supported(a)) return launch_la_tc(&a, 1, stream);
-  if (!a.bf16) return launch_core_type<false, true>(a, stream);
-  return a.out_f32 ? launch_core_type<true, true>(a, stream) : launch_core_type<true, false>(a, stream);
-}
-
-bool la_joint(const LaCore& a, const LaCore& b, const LaCore& c) {
-  return la_tc_supported(a) && la_tc_supported(b) && la_tc_supported(c) && a.KD == b.KD && a.KD == c.KD &&
-         a.VD == b.VD && a.VD == c.VD;
-}
-
-size_t la_joint_ws_bytes(const LaCore& a0) {
+size_t la_group_ws_bytes(const LaCore& a0, int n) {
   LaCore a = a0;
-  la_tc_plan(&a, sm_count(), 3);
-  return a.nseg > 1 ? sizeof(float) * (size_t)(a.b * a.H) * a.nseg * a.KD * a.VD : 0;
+  plan_core(&a, n);
+  return n * pass_ws_bytes(a);
 }
 
-cudaError_t launch_la_joint(LaCore* cores, void* ws, cudaStream_t stream) {
-  const size_t each = la_joint_ws_bytes(cores[0]) / sizeof(float);
-  for (int i = 0; i < 3; ++i) {
-    la_tc_plan(&cores[i], sm_count(), 3);
-    cores[i].ws = static_cast<float*>(ws) + i * each;
+cudaError_t launch_la_group(LaCores* job, int n, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  for (int i = 0; i < n; ++i) {
+    plan_core(&job->p[i], n);
+    job->p[i].ws = static_cast<float*>(ws) + i * (pass_ws_bytes(job->p[i]) / sizeof(float));
   }
-  return launch_la_tc(cores, 3, stream);
+  const LaCore& a = job->p[0];
+  if (n * pass_ws_bytes(a) > ws_bytes) return cudaErrorInvalidValue;
+  if (la_tc_supported(a)) return launch_la_tc(*job, n, stream);
+  if (!a.bf16) return launch_core_type<false, true>(*job, n, stream);
+  return a.out_f32 ? launch_core_type<true, true>(*job, n, stream) : launch_core_type<true, false>(*job, n, stream);
 }
 
-cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
-                               cudaStream_t stream) {
+cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* const* part, void* const* out,
+                               int n, cudaStream_t stream) {
   const int64_t n4 = rows * G * (D / 4);
   if (n4 == 0) return cudaSuccess;
   const int64_t grid = (n4 + 255) / 256;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const float4* p = reinterpret_cast<const float4*>(part);
-  if (bf16) la_head_sum_kernel<true><<<(unsigned)grid, 256, 0, stream>>>(n4, H, G, D / 4, p, out);
-  else la_head_sum_kernel<false><<<(unsigned)grid, 256, 0, stream>>>(n4, H, G, D / 4, p, out);
+  const float4* p0 = reinterpret_cast<const float4*>(part[0]);
+  const float4* p1 = reinterpret_cast<const float4*>(part[n - 1]);
+  const dim3 g((unsigned)grid, (unsigned)n);
+  if (bf16) la_head_sum_kernel<true><<<g, 256, 0, stream>>>(n4, H, G, D / 4, p0, out[0], p1, out[n - 1]);
+  else la_head_sum_kernel<false><<<g, 256, 0, stream>>>(n4, H, G, D / 4, p0, out[0], p1, out[n - 1]);
   return cudaGetLastError();
 }
 

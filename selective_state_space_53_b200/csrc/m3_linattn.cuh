@@ -108,19 +108,21 @@ __device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t n
 }
 
 // Launchers.
-cudaError_t launch_la_prefix(const LaCore& a, bool tc, cudaStream_t stream);  // entering states from end states
-size_t la_core_ws_bytes(const LaCore& a);  // scratch of the pass (plans its segments)
 bool la_tc_supported(const LaCore& a);     // the tensor-core form takes this pass
 void la_tc_plan(LaCore* a, int sms, int passes);
-// Up to three passes of the same sizes, planned alike, scratch in ws.
-cudaError_t launch_la_tc(const LaCore* cores, int n, cudaStream_t stream);
-// The gradients' passes may run as one launch (all on the tensor cores, N = P): then the scratch of each.
-bool la_joint(const LaCore& a, const LaCore& b, const LaCore& c);
-size_t la_joint_ws_bytes(const LaCore& a);
-cudaError_t launch_la_joint(LaCore* cores, void* ws, cudaStream_t stream);
-cudaError_t launch_la_core(LaCore a, void* ws, size_t ws_bytes, cudaStream_t stream);
-cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* part, void* out,
-                               cudaStream_t stream);
+// Passes that one launch can take together, up to three of them (the gradients of a layer): their kernels fill the
+// machine side by side, and a chain of launches is paid once.
+struct LaCores {
+  LaCore p[3];
+};
+bool la_alike(const LaCore& a, const LaCore& b);
+size_t la_group_ws_bytes(const LaCore& a, int n);  // scratch of n passes like this one (plans their segments)
+cudaError_t launch_la_group(LaCores* cores, int n, void* ws, size_t ws_bytes, cudaStream_t stream);
+cudaError_t launch_la_tc(const LaCores& cores, int n, cudaStream_t stream);                // planned, scratch set
+cudaError_t launch_la_prefix(const LaCores& cores, int n, bool tc, cudaStream_t stream);  // entering states from end states
+// out[i] (rows, G, D) = the sums over a group's heads of part[i] (rows, H, D), i < n <= 2
+cudaError_t launch_la_head_sum(int64_t rows, int H, int G, int D, int bf16, const float* const* part, void* const* out,
+                               int n, cudaStream_t stream);
 struct LaStep {
   int64_t b;
   int H, G, N, P, bf16;

@@ -795,19 +795,19 @@ cudaError_t launch_tc_mode(const LaJob& job, int n, cudaStream_t stream) {
 }
 
 template <int KD>
-cudaError_t launch_tc_kd(const LaCore* cores, int n, cudaStream_t stream) {
+cudaError_t launch_tc_kd(const LaCores& cores, int n, cudaStream_t stream) {
   LaJob job;
   for (int i = 0; i < n; ++i) {
     LaPass& p = job.p[i];
-    const LaCore& a = p.a = cores[i];
+    const LaCore& a = p.a = cores.p[i];
     if (!la_map(&p.q, a, a.q, a.hq, KD) || !la_map(&p.k, a, a.k, a.hk, KD) || !la_map(&p.v, a, a.v, a.hv, a.VD))
       return cudaErrorInvalidValue;
     if (a.out_f32) p.o = p.v;  // unused: fp32 outputs are written from registers
     else if (!la_map(&p.o, a, a.out, a.H, a.VD)) return cudaErrorInvalidValue;
   }
-  if (cores[0].nseg > 1) {
+  if (cores.p[0].nseg > 1) {
     cudaError_t e = launch_tc_mode<KD, 1>(job, n, stream);
-    for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_la_prefix(cores[i], true, stream);
+    if (e == cudaSuccess) e = launch_la_prefix(cores, n, true, stream);
     if (e != cudaSuccess) return e;
   }
   return launch_tc_mode<KD, 0>(job, n, stream);
@@ -840,8 +840,8 @@ void la_tc_plan(LaCore* a, int sms, int passes) {
   a->nseg = (int)((nch + segc - 1) / segc);
 }
 
-cudaError_t launch_la_tc(const LaCore* cores, int n, cudaStream_t stream) {
-  return cores[0].KD == 64 ? launch_tc_kd<64>(cores, n, stream) : launch_tc_kd<128>(cores, n, stream);
+cudaError_t launch_la_tc(const LaCores& cores, int n, cudaStream_t stream) {
+  return cores.p[0].KD == 64 ? launch_tc_kd<64>(cores, n, stream) : launch_tc_kd<128>(cores, n, stream);
 }
 
 }  // namespace m3

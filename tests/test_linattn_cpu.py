@@ -158,3 +158,19 @@ def test_pages_refuses_tensors():
         m3.Pages([])
     with pytest.raises(m3.M3Error):
         m3.Pages([torch.zeros(4, 8)])  # not on a CUDA device
+
+
+def test_calls_follow_the_tensors_device(monkeypatch):
+    """A call runs on the current stream of its tensors' device; with another device current, or a stream given,
+    it switches there first."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    assert m3._call_stream(0, None) == 1000
+    assert m3._call_stream(1, None) is None
+    assert m3._call_stream(0, object()) is None
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", lambda d: seen.append(("device", d)))
+    monkeypatch.setattr(torch.cuda, "stream", lambda st: seen.append(("stream", st)))
+    m3._elsewhere("cuda:1", None)
+    m3._elsewhere("cuda:1", "st")
+    assert seen == [("device", "cuda:1"), ("stream", "st")]
