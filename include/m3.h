@@ -327,7 +327,7 @@ m3_status m3_linattn_fwd(const m3_dims* dims, const void* q, const void* k, cons
                          float scale, const int32_t* lens, const float* state_in, float* state_out, int64_t npages,
                          const int32_t* pages, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
-/* One token of every sequence (dims->L is ignored): q_t, k_t (b, G, N), v_t, y_t (b, H, P).  Reads
+/* One token of every sequence (any valid dims->L): q_t, k_t (b, G, N), v_t, y_t (b, H, P).  Reads
  * and rewrites the states in place, in fp32 throughout.  Asynchronous on `stream`. */
 m3_status m3_linattn_step(const m3_dims* dims, const void* q_t, const void* k_t, const void* v_t,
                           const float* log_decay, float scale, float* state, int64_t npages, const int32_t* pages,

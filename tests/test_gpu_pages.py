@@ -228,3 +228,22 @@ def test_linear_attention_served_from_pages(graph):
     for s in layers:
         got = d(s)[:3]
         assert np.abs(got - S[1:]).max() <= 1e-5 * np.abs(S).max()
+
+
+def test_pool_past_32_bit_offsets():
+    """The last pages of a pool of 2.2e9 values: copies, prompts, tokens as in a pool of three pages."""
+    H, N, P, rows = 32, 128, 128, 4200
+    big = torch.empty(rows, H, N, P, device="cuda")  # only the pages named below are touched
+    small = torch.randn(3, H, N, P, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    last = [rows - 3, rows - 2, rows - 1]
+    big[rows - 3:] = small
+    for t, at in ((big, last), (small, [0, 1, 2])):
+        g = torch.Generator(device="cuda").manual_seed(2)
+        draw = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()  # noqa: E731
+        ld = -torch.rand(H, generator=g, device="cuda")
+        m3.Pages([t]).copy(_ints(at[:1]), _ints(at[2:]))
+        m3.linattn(draw(2, 150, H, N), draw(2, 150, H, N), draw(2, 150, H, P), ld, state=t, pages=_ints([at[2], at[1]]))
+        m3.linattn_step(draw(3, 1, N), draw(3, 1, N), draw(3, H, P), ld, t, pages=_ints(at))
+    torch.cuda.synchronize()
+    assert m3.m3_check() == 0
+    assert torch.equal(big[rows - 3:], small)
