@@ -471,8 +471,9 @@ int lanes_of(int KD) {
 // Columns and warps of a CTA: the value dim over as few CTAs of at most kLaWarps warps as it takes.
 int warps_of(const LaCore& a) {
   const int cpw = 128 / lanes_of(a.KD), need = (a.VD + cpw - 1) / cpw;
-  const int ctas = (need + kLaWarps - 1) / kLaWarps;
-  return (need + ctas - 1) / ctas;
+  const int ctas = (need + kLaWarps - 1) / kLaWarps, warps = (need + ctas - 1) / ctas;
+  // eight columns at least to a step: a CTA's columns start on 16 bytes in bf16 (above 128 rows a warp has four)
+  return cpw < 8 ? (warps + 1) & ~1 : warps;
 }
 int cols_of(const LaCore& a) { return warps_of(a) * (128 / lanes_of(a.KD)); }
 

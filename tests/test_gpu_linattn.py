@@ -92,6 +92,9 @@ SHAPES = [
     (2, 33, 4, 2, 16, 200, "bf16", [0, 33], True, None),
     (1, 500, 2, 1, 136, 48, "bf16", None, True, [0.0, -np.inf]),
     (1, 19, 24, 1, 64, 64, "bf16", None, False, None),
+    (1, 40, 2, 1, 192, 40, "bf16", None, True, None),
+    (2, 21, 2, 2, 8, 136, "bf16", [21, 5], True, None),
+    (1, 100, 1, 1, 256, 8, "bf16", None, True, None),
 ]
 
 
