@@ -312,9 +312,10 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  * shortest sequences and in the step.  With bf16 tensors, N, P in {64, 128} and more than 24 tokens
  * (gradients: 12) the products run on the tensor cores with fp32 accumulation, in chunks of 128
  * tokens: the weighted scores and the copy of the state that q meets are rounded to bf16; the state
- * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  There an infinity or NaN in a
- * token may also reach the other tokens of its chunk, earlier ones included (a masked score is zero,
- * and zero times infinity is not); tokens past a sequence's length never matter.
+ * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  With G < H the heads' shares
+ * of dq and dk are summed in fp32 but carry that rounding each: where they cancel, it stays.  An
+ * infinity or NaN in a token may also reach the other tokens of its chunk, earlier ones included (a
+ * masked score is zero, and zero times infinity is not); tokens past a sequence's length never matter.
  */
 
 /* Scratch bytes m3_linattn_fwd needs for these dims (0 when it needs none). */
