@@ -312,8 +312,10 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  * shortest sequences and in the step.  With bf16 tensors, N, P in {64, 128} and more than 24 tokens
  * (gradients: 12) the products run on the tensor cores with fp32 accumulation, in chunks of 128
  * tokens: the weighted scores and the copy of the state that q meets are rounded to bf16; the state
- * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  With G < H the heads' shares
- * of dq and dk are summed in fp32 but carry that rounding each: where they cancel, it stays.  An
+ * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  An output is off by at most 2^-8
+ * of the sum of the absolute values of its terms, beside its own rounding to bf16.  With G < H the heads'
+ * shares of dq and dk, which may cancel in their sum, keep two bf16 parts of each operand and are summed
+ * in fp32: off by at most 2^-14 of the terms' absolute values, and the final rounding.  An
  * infinity or NaN in a token may also reach the other tokens of its chunk, earlier ones included (a
  * masked score is zero, and zero times infinity is not); tokens past a sequence's length never matter.
  */

@@ -15,10 +15,21 @@
 // 64 bits; a pair's weight is one factor of its row times one of its column within 32 x 32 blocks,
 // both at most 1, so nothing overflows for any decay.
 //
-// Roundings: A' and the copy of S that q meets are bf16 (each moves the result by less than its own
-// final rounding to bf16 does).  The state is an fp32 result, so its update must not lose bits: the
-// weighted v enters as three bf16 parts (8 bits each: all 24 of the product) side by side as N = 192 columns
-// of one product, so k is read once for all three, and a^128 is a two-float constant.
+// Roundings: A' and the copy of S that q meets are bf16: an output is off by at most 2^-8 of the sum of
+// the absolute values of its terms, beside its own rounding to bf16.  Where the terms do not cancel the two are
+// alike (b2 L32768 H32 N = P = 128: relative 2-norm 2.3e-3 against 1.7e-3 of the final rounding alone), and
+// a second part of A' and S would cost the tensor pipe two more products a chunk and 16 KiB that a head of
+// 128 does not have.  The state is an fp32 result, so its update must not lose bits: the weighted v enters as
+// three bf16 parts (8 bits each: all 24 of the product) side by side as N = 192 columns of one product, so k is
+// read once for all three, and a^128 is a two-float constant.
+//
+// fp32 outputs (MODE 2) are a head's shares of a gradient that heads share: they are summed over the heads,
+// where they may cancel, so their operands keep more.  A' and S enter as two bf16 parts each (2^-16 of a value
+// is left), Yi and Ya are two products each into one accumulator, and an output is off by at most 2^-14 of its
+// terms.  No caller reads the state of such a pass, so its weighted v has two parts (the second rounded: 2^-15 is
+// left); the third part's shared memory then holds the low part of S and its accumulator columns that of A'.
+// With one valid token and twelve heads dq and dk were 3e-2 off (relative 2-norm) with one part each, 1.6e-3 with two,
+// the final rounding's own; the gradients at b4 L2048 H24 G1 N = P = 64 take 140 us, 108 with one part.
 //
 // Warp roles (20 warps; every mbarrier wait is bounded by %globaltimer):
 //   0      producer: TMA loads of q, k, v into two stages (128-byte swizzle)
@@ -99,9 +110,12 @@ struct LaCfg {
   static constexpr int OFF_MISC = OFF_BAR + LNBAR * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
   static constexpr uint32_t TM_A = 0, TM_AP = 128, TM_YA = 192, TM_YI = 256, TM_H = 320, TM_COLS = 512;
+  static constexpr uint32_t TM_AL = TM_H + 2 * LV;  // low part of A' (shares: the update has two parts)
+  static constexpr int OFF_SL = OFF_VT + 2 * LBLK;  // low part of S (shares)
   static constexpr uint32_t ID_A = idesc_bf16(128, 128, false, false);
   static constexpr uint32_t ID_Y = idesc_bf16(128, LV, false, true);
   static constexpr uint32_t ID_H = idesc_bf16(KD, 3 * LV, true, true);
+  static constexpr uint32_t ID_H2 = idesc_bf16(KD, 2 * LV, true, true);
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -205,6 +219,7 @@ struct LaJob {
   LaPass p[3];
 };
 
+// MODE 0: outputs in bf16; 1: the state pass of a segment; 2: some of the passes are shares (fp32 outputs).
 template <int KD, int MODE>
 __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_constant__ LaJob job) {
   const CUtensorMap& tmQ = job.p[blockIdx.y].q;
@@ -213,7 +228,9 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
   const CUtensorMap& tmO = job.p[blockIdx.y].o;
   const LaCore& a = job.p[blockIdx.y].a;
   using C = LaCfg<KD>;
-  constexpr bool FULL = MODE == 0;
+  constexpr bool FULL = MODE != 1;
+  const bool share = MODE == 2 && a.out_f32;  // (the outputs' code asks a.out_f32 itself: without that branch the
+                                              // bf16 form interleaves its blocks, 1.5 % slower at 32K)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // the warp index as a uniform value: addresses and branches that hang on it stay off the vector registers
@@ -235,7 +252,7 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
   auto sQ = [&](int s) { return sBase + (uint32_t)(s * C::STAGE); };
   auto sK = [&](int s) { return sBase + (uint32_t)(s * C::STAGE + C::TILE_K); };
   auto sV = [&](int s) { return sBase + (uint32_t)(s * C::STAGE + 2 * C::TILE_K); };
-  const uint32_t sVT = sBase + C::OFF_VT, sS = sBase + C::OFF_S;
+  const uint32_t sVT = sBase + C::OFF_VT, sS = sBase + C::OFF_S, sSL = sBase + C::OFF_SL;
 
   // ---- setup
   if (warp == L_MMA) {
@@ -387,6 +404,7 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
       const uint64_t dQ = sdesc(sQ(0), 16, 1024), dK = sdesc(sK(0), 16, 1024);          // K-major
       const uint64_t dKt = sdesc(sK(0), LBLK, 1024), dVm = sdesc(sV(0), LBLK, 1024);    // MN-major
       const uint64_t dS = sdesc(sS, LBLK, 1024), dVT = sdesc(sVT, LBLK, 1024);
+      const uint64_t dSL = sdesc(sSL, LBLK, 1024);
       auto stage = [&](int i) { return (uint64_t)((i & 1) * (C::STAGE >> 4)); };
       auto kstep = [](int k) { return (uint64_t)(((k >> 2) * LBLK + (k & 3) * 32) >> 4); };
       auto mstep = [](int k) { return (uint64_t)((k * 2048) >> 4); };
@@ -417,7 +435,7 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
         if (lead) {
 #pragma unroll
           for (int k = 0; k < LQ / 16; ++k)
-            mma_ss1(tmem + C::TM_H, dKt + stage(i) + mstep(k), dVT + mstep(k), C::ID_H, k > 0);
+            mma_ss1(tmem + C::TM_H, dKt + stage(i) + mstep(k), dVT + mstep(k), share ? C::ID_H2 : C::ID_H, k > 0);
           mma_commit1(&bar[LB_H]);
           mma_commit1(&bar[LB_FK + s]);
           if (!FULL) mma_commit1(&bar[LB_FV + s]);
@@ -432,6 +450,11 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
 #pragma unroll
             for (int k = 0; k < KD / 16; ++k)
               mma_ss1(tmem + C::TM_YI, dQ + stage(i) + kstep(k), dS + mstep(k), C::ID_Y, k > 0);
+            if (share) {
+#pragma unroll
+              for (int k = 0; k < KD / 16; ++k)
+                mma_ss1(tmem + C::TM_YI, dQ + stage(i) + kstep(k), dSL + mstep(k), C::ID_Y, 1);
+            }
             mma_commit1(&bar[LB_YI]);
           }
           __syncwarp();
@@ -442,6 +465,11 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
 #pragma unroll
             for (int k = 0; k < LQ / 16; ++k)
               mma_ts1(tmem + C::TM_YA, tmem + C::TM_AP + 8 * k, dVm + stage(i) + mstep(k), C::ID_Y, k > 0);
+            if (share) {
+#pragma unroll
+              for (int k = 0; k < LQ / 16; ++k)
+                mma_ts1(tmem + C::TM_YA, tmem + C::TM_AL + 8 * k, dVm + stage(i) + mstep(k), C::ID_Y, 1);
+            }
             mma_commit1(&bar[LB_Y]);
             mma_commit1(&bar[LB_FV + s]);
           }
@@ -483,6 +511,8 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
         for (int e = 0; e < 16; ++e) o[e] = 0u;
         if (d0 < 0) tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb0, o);
         if (d1 < 0) tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb1, o);
+        if (share && d0 < 0) tmem_st16(tmem + lane_base + C::TM_AL + 16 * cb0, o);
+        if (share && d1 < 0) tmem_st16(tmem + lane_base + C::TM_AL + 16 * cb1, o);
       }
       const float r1 = d1 > 0 ? sc * lds32(sPow + 4 * (a.rev ? 32 * d1 - lane : 32 * d1 - 31 + lane)) : 0.0f;
       for (int i = 0; i < n; ++i) {
@@ -490,7 +520,7 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
         const int nv = i == part ? nv_part : LQ;
         named_bar_sync(LN_SC, LN_THREADS);
         tc_fence_after();
-        auto finish = [&](int cb, uint32_t (&o)[16]) {
+        auto finish = [&](uint32_t to, int cb, uint32_t (&o)[16]) {
           if (32 * cb + 32 > nv) {  // columns past the length
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -498,35 +528,46 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
               else if (32 * cb + 2 * e + 1 >= nv) o[e] &= 0xffffu;
             }
           }
-          tmem_st16(tmem + lane_base + C::TM_AP + 16 * cb, o);
+          tmem_st16(tmem + lane_base + to + 16 * cb, o);
+        };
+        auto rest = [&](int cb, const float (&x)[32]) {  // what the rounding of a block left
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t hi = pack_bf16(x[2 * e], x[2 * e + 1]);
+            o[e] = pack_bf16(x[2 * e] - bf_lo(hi), x[2 * e + 1] - bf_hi(hi));
+          }
+          finish(C::TM_AL, cb, o);
         };
         if (d0 >= 0) {
           uint32_t v[32], o[16];
+          float x[32];
           tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb0, v);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            f2_split(f2_mul(f2_bits(v[2 * e], v[2 * e + 1]), W[e]), x0, x1);
-            o[e] = pack_bf16(x0, x1);
+            f2_split(f2_mul(f2_bits(v[2 * e], v[2 * e + 1]), W[e]), x[2 * e], x[2 * e + 1]);
+            o[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
           }
-          finish(cb0, o);
+          finish(C::TM_AP, cb0, o);
+          if (share) rest(cb0, x);
         }
         if (d1 >= 0) {
           uint32_t v[32], o[16];
+          float x[32];
           tmem_ld32(tmem + lane_base + C::TM_A + 32 * cb1, v);
           tmem_wait_ld();
           const uint64_t r2 = f2(r1, r1);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint4 u = lds128(sCol + 16 * e);
-            float x0, x1, x2, x3;
-            f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x0, x1);
-            f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x2, x3);
-            o[2 * e] = pack_bf16(x0, x1);
-            o[2 * e + 1] = pack_bf16(x2, x3);
+            f2_split(f2_mul(f2_bits(v[4 * e], v[4 * e + 1]), f2_mul(f2_bits(u.x, u.y), r2)), x[4 * e], x[4 * e + 1]);
+            f2_split(f2_mul(f2_bits(v[4 * e + 2], v[4 * e + 3]), f2_mul(f2_bits(u.z, u.w), r2)), x[4 * e + 2], x[4 * e + 3]);
+            o[2 * e] = pack_bf16(x[4 * e], x[4 * e + 1]);
+            o[2 * e + 1] = pack_bf16(x[4 * e + 2], x[4 * e + 3]);
           }
-          finish(cb1, o);
+          finish(C::TM_AP, cb1, o);
+          if (share) rest(cb1, x);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -639,7 +680,17 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
             f2_split(S[4 * c + e], lo, hi);
             o[e] = pack_bf16(lo, hi);
           }
-          sts128(sS + row * 128 + (((c + 4 * w) ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          const uint32_t to = row * 128 + (((c + 4 * w) ^ (row & 7)) << 4);
+          sts128(sS + to, make_uint4(o[0], o[1], o[2], o[3]));
+          if (share) {  // what the rounding left
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              f2_split(S[4 * c + e], lo, hi);
+              o[e] = pack_bf16(lo - bf_lo(o[e]), hi - bf_hi(o[e]));
+            }
+            sts128(sSL + to, make_uint4(o[0], o[1], o[2], o[3]));
+          }
         }
       }
       fence_async_smem();
@@ -647,7 +698,7 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
     };
 
     // ---- the weighted v of chunk i: three parts of 8 values; each part takes the upper 16 bits of what
-    // is left, 24 bits in all
+    // is left, 24 bits in all (shares: two parts, the second rounded)
     auto weight = [&](int i) {
       const int nv = i == part ? nv_part : LQ;
       return t < nv ? a.s_upd * lds32(sPow + 4 * (a.rev ? t + 1 : nv - 1 - t)) : 0.0f;
@@ -676,11 +727,13 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
           uint32_t b[4];
+          if (share && q == 2) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float lo, hi;
             f2_split(f[e], lo, hi);
-            b[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            if (share && q == 1) b[e] = pack_bf16(lo, hi);
+            else b[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
             if (q < 2)  // exact
               f[e] = f2_fma(f2(__uint_as_float(__float_as_uint(lo) & 0xffff0000u),
                                __uint_as_float(__float_as_uint(hi) & 0xffff0000u)), minus, f[e]);
@@ -712,7 +765,12 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
         uint32_t x[8], y[8], z[8];
         tmem_ld8(tmem + lane_base + C::TM_H + LSC * w + 8 * c, x);
         tmem_ld8(tmem + lane_base + C::TM_H + LV + LSC * w + 8 * c, y);
-        tmem_ld8(tmem + lane_base + C::TM_H + 2 * LV + LSC * w + 8 * c, z);
+        if (share) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = 0u;
+        } else {
+          tmem_ld8(tmem + lane_base + C::TM_H + 2 * LV + LSC * w + 8 * c, z);
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -788,7 +846,7 @@ cudaError_t launch_tc_mode(const LaJob& job, int n, cudaStream_t stream) {
   const cudaError_t e = attr.ensure(kern, LaCfg<KD>::SMEM);
   if (e != cudaSuccess) return e;
   const LaCore& a = job.p[0].a;
-  const int64_t grid = a.b * a.H * (a.VD / LV) * (MODE == 0 ? a.nseg : a.nseg - 1);
+  const int64_t grid = a.b * a.H * (a.VD / LV) * (MODE == 1 ? a.nseg - 1 : a.nseg);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   kern<<<dim3((unsigned)grid, (unsigned)n), L_THREADS, LaCfg<KD>::SMEM, stream>>>(job);
   return cudaGetLastError();
@@ -810,6 +868,8 @@ cudaError_t launch_tc_kd(const LaCores& cores, int n, cudaStream_t stream) {
     if (e == cudaSuccess) e = launch_la_prefix(cores, n, true, stream);
     if (e != cudaSuccess) return e;
   }
+  for (int i = 0; i < n; ++i)
+    if (cores.p[i].out_f32) return launch_tc_mode<KD, 2>(job, n, stream);
   return launch_tc_mode<KD, 0>(job, n, stream);
 }
 
