@@ -405,7 +405,8 @@ def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y
     q, k (b, L, G, N), v (b, L, H, P) bf16 or fp32, G dividing H; log_decay (H) fp32; scale: N ** -0.5
     if not given; lens (b) int32: the lengths of a padded batch.  state (b, H, N, P) fp32, updated in
     place, or with pages (b) int32 the rows of a pool (npages, H, N, P); without it the sequences are
-    fresh.  Returns (y, state)."""
+    fresh.  workspace: a contiguous tensor of m3_linattn_workspace_size bytes on the same device, else
+    one is allocated.  Returns (y, state)."""
     import torch
     what = "linattn"
     dims = _la_dims(what, q, k, v, log_decay, False)
@@ -417,6 +418,8 @@ def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y
     rows = dims.b if state is None else _la_rows(what, dims, state, pages, dev)
     if y is not None:
         _expect(what, "y", y, v.shape, v.dtype, dev)
+    if workspace is not None:  # any type; its bytes are checked by the library
+        _expect(what, "workspace", workspace, workspace.shape, workspace.dtype, dev)
     raw = _call_stream(dev.index, stream)
     if raw is None:
         with _elsewhere(dev, stream):
