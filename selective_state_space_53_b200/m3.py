@@ -299,8 +299,11 @@ def scan_backward(dims: Dims, dev: dict, state0: State, dy, dh_final=None, strea
 
 def _call_stream(index, stream):
     """Raw handle of the stream a call on tensors of CUDA device `index` runs on: `stream`, or the device's
-    current one.  None when the call has to switch to that device or stream first (``_elsewhere``)."""
+    current one.  None when the call has to switch to that device or stream first (``_elsewhere``).  A stream
+    of another device is refused: it could not order the work that the caller asks it to."""
     import torch
+    if stream is not None and getattr(stream, "device_index", index) != index:
+        raise M3Error(-1, f"stream is on cuda:{stream.device_index}, expected the tensors' device cuda:{index}")
     if stream is None and torch._C._cuda_getDevice() == index:
         return torch._C._cuda_getCurrentRawStream(index)
     return None

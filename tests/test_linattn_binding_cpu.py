@@ -13,6 +13,9 @@ class Fake:
     def __init__(self, *shape, dtype=torch.bfloat16, device="cuda:0", contiguous=True):
         self.shape, self.dtype, self.device, self._c = torch.Size(shape), dtype, torch.device(device), contiguous
 
+    def __getitem__(self, i):
+        return Fake(*self.shape[1:], dtype=self.dtype, device=self.device)
+
     def dim(self):
         return len(self.shape)
 
@@ -53,3 +56,44 @@ def test_workspace_refused(closed, workspace):
     with pytest.raises(m3.M3Error) as e:
         m3.linattn(**_prompt(), workspace=workspace)
     assert e.value.code == -1 and "workspace" in str(e.value)
+
+
+class Stream:
+    def __init__(self, index):
+        self.device_index, self.device = index, torch.device("cuda", index)
+
+
+def _pool():
+    return m3.Pages([Fake(4, 8, **F32)], Fake(4, **I32))
+
+
+@pytest.mark.parametrize("call", [
+    lambda s: m3.linattn(**_prompt(), stream=s),
+    lambda s: m3.linattn_step(Fake(B, G, N), Fake(B, G, N), Fake(B, H, P), Fake(H, **F32), Fake(B, H, N, P, **F32),
+                              y=Fake(B, H, P), stream=s),
+    lambda s: m3.linattn_backward(Fake(B, T, G, N), Fake(B, T, G, N), Fake(B, T, H, P), Fake(H, **F32),
+                                  Fake(B, T, H, P), stream=s),
+    lambda s: _pool().copy(Fake(2, **I32), Fake(2, **I32), stream=s),
+    lambda s: _pool().fork(Fake(2, **I32), stream=s),
+    lambda s: _pool().free(Fake(2, **I32), stream=s),
+    lambda s: _pool().compact(stream=s)], ids=["linattn", "step", "backward", "copy", "fork", "free", "compact"])
+def test_stream_of_another_device_refused(closed, monkeypatch, call):
+    """Such a stream cannot order work on the tensors' device: running elsewhere instead would leave a caller that
+    waits for it with unfinished outputs."""
+    entered = []
+
+    class Context:
+        def __init__(self, target):
+            self.target = target
+
+        def __enter__(self):
+            entered.append(self.target)
+
+        def __exit__(self, *exc):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    with pytest.raises(m3.M3Error) as e:
+        call(Stream(1))
+    assert e.value.code == -1 and "stream" in str(e.value) and not entered
