@@ -506,6 +506,8 @@ class Pages:
             raise M3Error(-1, f"Pages: {len(bufs)} buffers, expected 1 to {PAGES_MAX_BUF}")
         self.device = bufs[0].device
         self.npages = bufs[0].shape[0] if bufs[0].dim() else 0
+        if self.npages > 0x7fffffff:
+            raise M3Error(-1, f"Pages: {self.npages} pages, expected fewer than 2^31")
         s = PagesStruct(self.npages, len(bufs))
         for j, t in enumerate(bufs):
             if t.dim() < 2:

@@ -97,3 +97,11 @@ def test_stream_of_another_device_refused(closed, monkeypatch, call):
     with pytest.raises(m3.M3Error) as e:
         call(Stream(1))
     assert e.value.code == -1 and "stream" in str(e.value) and not entered
+
+
+@pytest.mark.parametrize("npages", [1 << 31, (1 << 32) + 5])
+def test_pool_of_more_pages_than_an_index_refused(closed, npages):
+    """Page indices are 32-bit: a larger pool would be taken for a smaller one."""
+    with pytest.raises(m3.M3Error) as e:
+        m3.Pages([Fake(npages, 8, **F32)], Fake(npages, **I32))
+    assert e.value.code == -1
