@@ -170,12 +170,15 @@ WsLayout ws_layout(const m3_dims* dims) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Dims of the linear attention: R = 1, no flags, and element offsets of every tensor within 63 bits.
+// Dims of the linear attention: R = 1, no flags, and the bytes of every tensor and of the scratch within 63 bits:
+// the heads' shares of dq and dk are 8 b L H N bytes, the segments' states below 2^57.
 m3_status check_la_dims(const m3_dims* d) {
   m3_status st = check_ranges(d);
   if (st != M3_OK) return st;
   if (d->R != 1 || d->flags != 0) return M3_ERR_DIMS;
   if (d->L > (int64_t)0x7fffff00) return M3_ERR_DIMS;  // a token index is a 32-bit tile coordinate
+  if (d->b > (int64_t)0x7fffffff / d->H) return M3_ERR_DIMS;
+  if (d->b * d->H * d->L > INT64_MAX / (16 * (d->N > d->P ? d->N : d->P))) return M3_ERR_DIMS;
   return M3_OK;
 }
 

@@ -105,3 +105,27 @@ def test_pool_of_more_pages_than_an_index_refused(closed, npages):
     with pytest.raises(m3.M3Error) as e:
         m3.Pages([Fake(npages, 8, **F32)], Fake(npages, **I32))
     assert e.value.code == -1
+
+
+@pytest.fixture(scope="module")
+def library():
+    from selective_state_space_53_b200 import build
+    build.build()
+    return m3.lib()
+
+
+@pytest.mark.parametrize("b,L,H,N,P", [
+    (1 << 10, 0x7fffff00, 1 << 20, 256, 256),   # b L H N 4 bytes = 2^71
+    (1, 0x7fffff00, 0x7fffffff, 16, 8),         # 2^68
+    (1 << 61, 1, 8, 16, 8),                     # b H = 2^64
+    ((1 << 62) + 1, 1, 4, 16, 8)])
+def test_sizes_past_63_bits_refused(library, b, L, H, N, P):
+    """Byte counts and offsets that do not fit 63 bits: a wrapped workspace size would let the kernels write past it."""
+    import ctypes
+    d, n, at = m3.make_dims(b, L, H, P, N, 1, 1, "bf16", chunk=0), ctypes.c_size_t(), ctypes.c_void_p(1 << 24)
+    assert library.m3_linattn_workspace_size(ctypes.byref(d), ctypes.byref(n)) == -1
+    assert library.m3_linattn_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)) == -1
+    r = ctypes.byref(d)
+    assert library.m3_linattn_fwd(r, at, at, at, at, 1.0, None, None, None, 0, None, at, None, 0, None) == -1
+    assert library.m3_linattn_bwd(r, at, at, at, at, 1.0, None, None, at, None, at, at, at, None, None, 0, None) == -1
+    assert library.m3_linattn_step(r, at, at, at, at, 1.0, at, 0, None, at, None) == -1
