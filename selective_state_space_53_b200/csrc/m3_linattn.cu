@@ -13,9 +13,11 @@
 // and leaves its end state, a prefix pass turns the end states into entering states, and the full pass
 // starts from those.
 //
-// g itself is rounded to fp32, and a product of d of them is off by up to d 2^-25: every 16 tokens
-// the state is multiplied by e^{16 log_decay} / g^16, taken in 64 bits, which leaves at most the
-// rounding of 16 factors.
+// g itself is rounded to fp32, and a product of d of them is off by up to d 2^-24, all one way.  So the first
+// token of every block of n <= 16 multiplies the state by g (1 + e + r) in g's place, e = e^{n log_decay} / g^n - 1
+// taken in 64 bits and r what the rounding of that factor left in the blocks before: a call's decay over any
+// number of blocks is off by half a step (2^-24) beside the factors within the last block, for a few operations a block.
+// (Adding S e to k v^T at the first token, which leaves no rest at all, took 8 to 10 % more time.)
 #include "m3_linattn.cuh"
 #include "m3_ptx.cuh"
 
@@ -70,15 +72,23 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_con
   const int len = page < 0 ? 0 : la_len(a, bi);
   const SegSpan sp = la_span(a, seg, len);
   const float ld = a.log_decay[h];
-  // g and e^{16 log_decay} / g^16, by one warp (64-bit exponentials are slow to issue)
-  __shared__ float factors[2];
+  // g and e^{n log_decay} / g^n - 1 of a full block and of the segment's last one, by one warp (64-bit exponentials
+  // are slow to issue)
+  __shared__ float factors[4];
   if (warp == 0) {
-    const double w = la_pow(ld, lane == 0 ? 1 : kTB);
-    double gp = (double)(float)__shfl_sync(kFull, w, 0);
-    if (lane == 0) factors[0] = (float)w;
+    const int e = lane == 0 ? 1 : lane == 1 ? kTB : (sp.tb - sp.ta) % kTB;
+    const double w = la_pow(ld, e);
+    double gi = (double)(float)__shfl_sync(kFull, w, 0), gp = 1.0;
+    if (lane == 0) {
+      factors[0] = (float)w;
+      factors[3] = w > 1e-30 ? (float)(1.0 / w) : 0.0f;
+    }
 #pragma unroll
-    for (int i = 1; i < kTB; i *= 2) gp *= gp;
-    if (lane == 1) factors[1] = gp > 1e-30 ? (float)(w / gp) : 1.0f;
+    for (int i = 1; i <= kTB; i *= 2) {
+      if (e & i) gp *= gi;
+      gi *= gi;
+    }
+    if (lane == 1 || lane == 2) factors[lane] = gp > 1e-30 ? (float)(w / gp - 1.0) : 0.0f;
   }
 
   // ---- the state entering the segment: rows 4 (ln + LN j) + e as pairs, columns cb..cb+3
@@ -139,7 +149,8 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_con
   if (a.KD < KDP || ncol < cols)
     for (int i = tid; i < 2 * bufsz * E / 16; i += nthr) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const float g = factors[0], corr = factors[1];
+  const float g = factors[0], ginv = factors[3];
+  float left = 0.0f;  // of the decays' roundings so far, relative
   const int ntok = sp.tb - sp.ta;
   const int nblk = (ntok + kTB - 1) / kTB;
   const int gq = h / (a.H / a.hq), gk = h / (a.H / a.hk), gv = h / (a.H / a.hv);
@@ -184,9 +195,13 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_con
     const T* bq = buf + s * bufsz + 4 * ln;
     const T* bk = bq + kTB * KDP;
     const T* bv = buf + s * bufsz + 2 * kTB * KDP + cb;
+    // the decay of the block's first token
+    const bool plain = first && ib == 0;
+    const float g1 = plain ? 1.0f : g, want = left + factors[nt == kTB ? 1 : 2], gh = fmaf(g1, want, g1);
+    left = want - (gh - g1) * (plain ? 1.0f : ginv);
     // one token: the state's update, and this thread's share of the four readouts
-    auto walk = [&](int t, float (&y)[4]) {
-      const float gt = (first && ib == 0 && t == 0) ? 1.0f : g;
+    auto walk = [&](int t, float (&y)[4], bool head) {
+      const float gt = head ? gh : g;
       const uint64_t g2 = f2(gt, gt);
       const float4 v4 = row4<BF16>(bv, t * cols);
       const uint64_t v2[4] = {f2(v4.x * u, v4.x * u), f2(v4.y * u, v4.y * u), f2(v4.z * u, v4.z * u),
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_con
     for (; t + 4 <= nt; t += 4) {
       float y[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) walk(t + i, y[i]);
+      for (int i = 0; i < 4; ++i) walk(t + i, y[i], i == 0 && t == 0);
       if constexpr (FULL) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) reduce(y[i]);
@@ -264,18 +279,11 @@ __global__ void __launch_bounds__(32 * kLaWarps) la_core_kernel(const __grid_con
 #pragma unroll 1
     for (; t < nt; ++t) {
       float y[4];
-      walk(t, y);
+      walk(t, y, t == 0);
       if constexpr (FULL) {
         reduce(y);
         keep(t, y);
       }
-    }
-    if (nt == kTB) {
-      const uint64_t c2 = f2(corr, corr);
-#pragma unroll
-      for (int rp = 0; rp < 4; ++rp)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) S[rp][c] = f2_mul(S[rp][c], c2);
     }
     __syncthreads();  // the block's readouts are complete, its operands read
     if constexpr (FULL) {
@@ -411,7 +419,9 @@ __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, i
     k[i] = n < a.N ? load_in<BF16>(a.k, kq + n) : 0.0f;
     q[i] = n < a.N ? load_in<BF16>(a.q, kq + n) : 0.0f;
   }
-  const float g = (float)exp((double)a.log_decay[h]);
+  // the decay as two floats: a long memory multiplies it in once a token
+  const double gd = exp((double)a.log_decay[h]);
+  const float g = (float)gd, gl = (float)(gd - (double)g);
   if (a.pages && la_page_block(a.pages, a.npages, bi, a.status) < 0) {
     if (on && rg == 0)
 #pragma unroll
@@ -422,10 +432,10 @@ __global__ void __launch_bounds__(kStepThreads) la_step_kernel(const LaStep a, i
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int n = rg + RG * i;
-    s[i].x = fmaf(g, s[i].x, k[i] * v[0]);
-    s[i].y = fmaf(g, s[i].y, k[i] * v[1]);
-    s[i].z = fmaf(g, s[i].z, k[i] * v[2]);
-    s[i].w = fmaf(g, s[i].w, k[i] * v[3]);
+    s[i].x = fmaf(g, s[i].x, fmaf(gl, s[i].x, k[i] * v[0]));
+    s[i].y = fmaf(g, s[i].y, fmaf(gl, s[i].y, k[i] * v[1]));
+    s[i].z = fmaf(g, s[i].z, fmaf(gl, s[i].z, k[i] * v[2]));
+    s[i].w = fmaf(g, s[i].w, fmaf(gl, s[i].w, k[i] * v[3]));
     if (on && n < a.N) __stcs(reinterpret_cast<float4*>(S + (int64_t)n * a.P), s[i]);
     y.x = fmaf(q[i], s[i].x, y.x);
     y.y = fmaf(q[i], s[i].y, y.y);
