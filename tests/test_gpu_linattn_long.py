@@ -36,13 +36,16 @@ def _states(rows, n, seed):
     return 10.0 ** (3 + u) * torch.where(torch.rand(u.shape, generator=g, device="cuda") < 0.5, -1.0, 1.0), g
 
 
-def test_long_walk():
-    """A prompt, and the gradient of its first state, walked token by token in one piece."""
-    b, L, n = 1200, 16384, 8
+@pytest.mark.parametrize("b,n,dtype", [(1200, 8, "f32"), (148, 64, "bf16")])
+def test_long_walk(b, n, dtype):
+    """A prompt, and the gradient of its first state, in one piece: token by token, and in chunks of 128 on the tensor
+    cores (fewer roundings)."""
+    L = 16384
     s, g = _states(b, n, 1)
-    q, k, v = (torch.randn(b, L, 1, n, generator=g, device="cuda") for _ in range(3))
+    q, k, v = (torch.randn(b, L, 1, n, generator=g, device="cuda").to(torch.float32 if dtype == "f32" else
+                                                                      torch.bfloat16) for _ in range(3))
     ld = torch.tensor([LD], device="cuda")
-    assert m3.m3_linattn_workspace_size(m3.make_dims(b, L, 1, n, n, 1, 1, "f32")) == 0  # not cut into segments
+    assert m3.m3_linattn_workspace_size(m3.make_dims(b, L, 1, n, n, 1, 1, dtype)) == 0  # not cut into segments
     a = torch.exp(ld.double() * torch.arange(L - 1, -1, -1, device="cuda").double())[None, :, None]
     decay = math.exp(float(ld.double()) * L)
     want = decay * s.double()[:, 0] + (k[:, :, 0].double() * a).transpose(1, 2) @ v[:, :, 0].double()
