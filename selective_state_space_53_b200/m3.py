@@ -369,6 +369,11 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw(stream):
+    """Raw handle of a stream, given as one already, as a torch stream or not at all (the current one)."""
+    return stream if stream.__class__ is int else _stream(stream)
+
+
 def m3_linattn_workspace_size(dims: Dims) -> int:
     n = ctypes.c_size_t()
     _check(lib().m3_linattn_workspace_size(ctypes.byref(dims), ctypes.byref(n)), "m3_linattn_workspace_size")
@@ -378,14 +383,14 @@ def m3_linattn_workspace_size(dims: Dims) -> int:
 def m3_linattn_fwd(dims: Dims, q, k, v, log_decay, scale, lens, state_in, state_out, npages, pages, y,
                    workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().m3_linattn_fwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), scale, _ptr(lens),
-                                _ptr(state_in), _ptr(state_out), npages, _ptr(pages), _ptr(y), _ptr(workspace),
-                                ws_bytes, _stream(stream)), "m3_linattn_fwd")
+    _check(lib().m3_linattn_fwd(ctypes.byref(dims), _adr(q), _adr(k), _adr(v), _adr(log_decay), scale, _adr(lens),
+                                _adr(state_in), _adr(state_out), npages, _adr(pages), _adr(y), _adr(workspace),
+                                ws_bytes, _raw(stream)), "m3_linattn_fwd")
 
 
 def m3_linattn_step(dims: Dims, q_t, k_t, v_t, log_decay, scale, state, npages, pages, y_t, stream=None):
-    _check(lib().m3_linattn_step(ctypes.byref(dims), _ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(log_decay), scale,
-                                 _ptr(state), npages, _ptr(pages), _ptr(y_t), _stream(stream)), "m3_linattn_step")
+    _check(lib().m3_linattn_step(ctypes.byref(dims), _adr(q_t), _adr(k_t), _adr(v_t), _adr(log_decay), scale,
+                                 _adr(state), npages, _adr(pages), _adr(y_t), _raw(stream)), "m3_linattn_step")
 
 
 def m3_linattn_bwd_workspace_size(dims: Dims) -> int:
@@ -397,9 +402,9 @@ def m3_linattn_bwd_workspace_size(dims: Dims) -> int:
 def m3_linattn_bwd(dims: Dims, q, k, v, log_decay, scale, lens, state_in, dy, dstate_out, dq, dk, dv, dstate_in,
                    workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().m3_linattn_bwd(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), scale, _ptr(lens),
-                                _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv),
-                                _ptr(dstate_in), _ptr(workspace), ws_bytes, _stream(stream)), "m3_linattn_bwd")
+    _check(lib().m3_linattn_bwd(ctypes.byref(dims), _adr(q), _adr(k), _adr(v), _adr(log_decay), scale, _adr(lens),
+                                _adr(state_in), _adr(dy), _adr(dstate_out), _adr(dq), _adr(dk), _adr(dv),
+                                _adr(dstate_in), _adr(workspace), ws_bytes, _raw(stream)), "m3_linattn_bwd")
 
 
 def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y=None, workspace=None, stream=None):
@@ -435,10 +440,8 @@ def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y
     if workspace is None:
         n = m3_linattn_workspace_size(dims)
         workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().m3_linattn_fwd(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                dims.N ** -0.5 if scale is None else scale, _adr(lens), _adr(state), out.data_ptr(),
-                                rows, _adr(pages), y.data_ptr(), _adr(workspace), ws_bytes, raw), "m3_linattn_fwd")
+    m3_linattn_fwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state, out, rows, pages,
+                   y, workspace, raw)
     return y, out
 
 
@@ -458,9 +461,7 @@ def linattn_step(q, k, v, log_decay, state, scale=None, pages=None, y=None, stre
             return linattn_step(q, k, v, log_decay, state, scale, pages, y)
     if y is None:
         y = torch.empty_like(v)
-    _check(lib().m3_linattn_step(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                 dims.N ** -0.5 if scale is None else scale, state.data_ptr(), rows, _adr(pages),
-                                 y.data_ptr(), raw), "m3_linattn_step")
+    m3_linattn_step(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, state, rows, pages, y, raw)
     return y
 
 
@@ -486,10 +487,8 @@ def linattn_backward(q, k, v, log_decay, dy, scale=None, lens=None, state0=None,
            "dstate0": torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)}
     n = m3_linattn_bwd_workspace_size(dims)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _check(lib().m3_linattn_bwd(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                dims.N ** -0.5 if scale is None else scale, _adr(lens), _adr(state0), dy.data_ptr(),
-                                _adr(dstate), *[out[g].data_ptr() for g in ("dq", "dk", "dv", "dstate0")], _adr(ws), n,
-                                raw), "m3_linattn_bwd")
+    m3_linattn_bwd(dims, q, k, v, log_decay, dims.N ** -0.5 if scale is None else scale, lens, state0, dy, dstate,
+                   *[out[g] for g in ("dq", "dk", "dv", "dstate0")], ws, raw)
     return out
 
 
