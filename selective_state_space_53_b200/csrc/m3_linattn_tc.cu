@@ -54,7 +54,6 @@
 // of shared-memory traffic: what bounds it is the latency of the SIMT tasks between the products (40 % of
 // the issue slots are used), not a pipe.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "m3_linattn.cuh"
 #include "m3_ptx.cuh"
@@ -812,22 +811,9 @@ __global__ void __launch_bounds__(L_THREADS, 1) la_tc_kernel(const __grid_consta
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 la_encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 // (b, L, heads, D) bf16 in boxes of 64 columns x 128 tokens of one head; tokens past L read as zero.
 bool la_map(CUtensorMap* m, const LaCore& a, const void* base, int heads, int D) {
-  auto fn = la_encode_fn();
+  auto fn = tma_encode_fn();
   if (!fn) return false;
   const cuuint64_t row = (cuuint64_t)D * 2, tok = row * heads;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)a.L, (cuuint64_t)a.b};

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -245,4 +246,8 @@ __device__ __forceinline__ void sincos_reduced(float x, float* s, float* c) {
 }
 
 }  // namespace
+
+// The driver's tensor map encoder, null if it has none (m3_scan_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn();
+
 }  // namespace m3
