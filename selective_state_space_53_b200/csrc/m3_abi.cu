@@ -197,9 +197,7 @@ m3::LaCore la_forward(const m3_dims* d) {
   a.s_upd = a.s_out = 1.0f;
   a.s_i = d->P;
   a.s_j = 1;
-  // Up to 24 tokens the recurrent core is quicker (b1 H24 N = P = 64: 3.9 to 8.1 us against 8.6; b64: 18 to 40
-  // against 89); the gradients' three passes up to 12 (b8 H32 64: 34 us against 57, b1 H24: 24 against 16).
-  a.tc_from = 25;
+  a.tc_from = m3::la_tc_from(a, 1, false);
   return a;
 }
 
@@ -214,7 +212,6 @@ LaBwd la_backward(const m3_dims* d) {
   LaBwd w;
   w.dv = la_forward(d);
   w.dv.rev = 1;
-  w.dv.tc_from = 13;
   w.dq = w.dv;
   w.dq.rev = 0;
   w.dq.KD = d->P;
@@ -224,6 +221,9 @@ LaBwd la_backward(const m3_dims* d) {
   w.dq.s_i = 1;
   w.dq.s_j = d->P;
   if (d->G < d->H) w.dq.out_f32 = 1;
+  const bool square = d->N == d->P;  // the three passes are alike then
+  w.dq.tc_from = m3::la_tc_from(w.dq, square ? 3 : 2, d->G < d->H);
+  w.dv.tc_from = m3::la_tc_from(w.dv, square ? 3 : 1, d->G < d->H);
   w.dk = w.dq;
   w.dk.rev = 1;
   w.first = m3::la_alike(w.dq, w.dv) ? 3 : 2;

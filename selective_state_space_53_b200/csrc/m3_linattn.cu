@@ -561,6 +561,19 @@ cudaError_t launch_la_prefix(const LaCores& job, int n, bool tc, cudaStream_t st
   return cudaGetLastError();
 }
 
+// A chunk costs the tensor cores the same for one token as for 128, 9 us a wave of CTAs at 64 rows and 12 at 128, the
+// recurrent core 4 to 7 us and 0.2 to 0.3 a token while the SMs have room for its warps.  Measured, recurrent against
+// tensor cores in us: one wave, b1 H24 64/64 at L16 7.4 and 9.0, L32 11 and 9; 128/128 at L16 10.5 and 12.4, L32 15
+// and 12.4.  More waves: b32 H32 64/64 at L48 49 and 60, L64 62 and 61 (b8: 19 and 18, 35 and 19); 128/128 at L32
+// 143 and 160, L48 191 and 162 (b8: 44 and 47, 57 and 47).  Gradients of own heads likewise: b1 H24 64/64 at L16 7.2
+// and 9.4, b32 H32 at L48 130 and 146, L64 168 and 148; 128/128 b8 H32 at L32 96 and 92.  Gradients of shared heads
+// take the recurrent core two launches and a sum: b1 H24 G1 64/64 at L8 15 and 15, L16 19 and 14; 128/128 20 and 19
+// at L12; with more waves b32 H32 G1 64/64 at L48 142 and 172, 128/128 b8 H32 G1 at L32 105 and 109.
+int la_tc_from(const LaCore& a, int passes, bool shares) {
+  if (a.b * a.H * ((a.VD + 63) / 64) * passes > sm_count()) return a.KD <= 64 ? 49 : 33;
+  return shares ? 13 : 25;
+}
+
 bool la_alike(const LaCore& a, const LaCore& b) {
   const bool tc = la_tc_supported(a);
   return tc == la_tc_supported(b) && a.KD == b.KD && a.VD == b.VD && (tc || a.out_f32 == b.out_f32);

@@ -109,6 +109,7 @@ __device__ __forceinline__ int64_t la_page_block(const int32_t* pages, int64_t n
 
 // Launchers.
 bool la_tc_supported(const LaCore& a);     // the tensor-core form takes this pass
+int la_tc_from(const LaCore& a, int passes, bool shares);  // the fewest tokens for which it should (LaCore::tc_from)
 void la_tc_plan(LaCore* a, int sms, int passes);
 // Passes that one launch can take together, up to three of them (the gradients of a layer): their kernels fill the
 // machine side by side, and a chain of launches is paid once.

@@ -218,3 +218,25 @@ def test_calls_run_on_the_stream_they_are_asked_to(name, given):
     got, want = _late(name, torch.cuda.Stream(), given)
     assert len(got) == len(want) and all(torch.equal(x, y) for x, y in zip(got, want))
     assert m3.m3_check() == 0
+
+
+@pytest.mark.parametrize("b,L,H,G,N,P", [(32, 40, 32, 1, 64, 64), (16, 32, 16, 16, 128, 128)])
+def test_short_sequences_of_many_heads_keep_fp32(b, L, H, G, N, P):
+    """Below the length from which a wave of chunks pays, bf16 operands meet fp32 arithmetic: an output is off by its
+    own rounding and by fp32 sums."""
+    dev, _ = draw(b, L, H, G, N, P, "bf16", seed=26)
+    ops = [dev[n] for n in ("q", "k", "v", "ld")]
+    absolute = [x.abs() for x in ops[:3]]
+    c = 2 * (2 * L + N + P) + 512 + H // G
+    y, s = m3.linattn(*ops, state=dev["s"].clone())
+    ref = host(*forward64(*ops, N ** -0.5, None, dev["s"]))
+    mag = host(*forward64(*absolute, dev["ld"], N ** -0.5, None, dev["s"].abs()))
+    check("y", y, ref[0], mag[0], c, "bf16")
+    check("state", s, ref[1], mag[1], c)
+    g = m3.linattn_backward(*ops, dev["dy"], state0=dev["s"], dstate=dev["ds"])
+    ref = host(*backward64(*ops, N ** -0.5, dev["dy"], None, dev["s"], dev["ds"]))
+    mag = host(*backward64(*absolute, dev["ld"], N ** -0.5, dev["dy"].abs(), None, dev["s"].abs(), dev["ds"].abs()))
+    for name, want, m in zip(("dq", "dk", "dv"), ref, mag):
+        check(name, g[name], want, m, c, "bf16")
+    check("dstate0", g["dstate0"], ref[3], mag[3], c)
+    assert m3.m3_check() == 0
