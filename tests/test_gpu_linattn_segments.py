@@ -118,7 +118,7 @@ def test_prompts_in_segments(b, L, H, G, N, P, dtype, lens, state, decay):
 
 @pytest.mark.parametrize("b,L,H,G,N,P,dtype,lens,state,decay", [
     (1, 2100, 8, 8, 128, 128, "bf16", [1411], True, None),
-    (2, 1700, 8, 8, 64, 64, "bf16", [1700, 700], True, [0.0, -1e-4, -0.05, -np.inf]),
+    (2, 2100, 6, 6, 64, 64, "bf16", [2100, 700], True, [0.0, -1e-4, -0.05, -np.inf]),
     (1, 4173, 6, 2, 64, 128, "bf16", None, True, None),
     (3, 1700, 4, 1, 128, 64, "bf16", [0, 1537, 1025], True, None),
     (4, 1200, 16, 16, 64, 64, "f32", [1200, 0, 601, 16], True, None)])
@@ -146,7 +146,7 @@ def test_gradients_in_segments(b, L, H, G, N, P, dtype, lens, state, decay):
     check("dstate0", g["dstate0"], ref[3], mag[3], c)
 
 
-@pytest.mark.parametrize("L,H,G,N,P,dtype", [(1700, 6, 1, 128, 128, "bf16"), (1500, 6, 2, 24, 40, "f32")])
+@pytest.mark.parametrize("L,H,G,N,P,dtype", [(2500, 3, 1, 128, 128, "bf16"), (1500, 6, 2, 24, 40, "f32")])
 def test_pages_in_segments(L, H, G, N, P, dtype):
     """Prompts cut into segments on rows of a pool: padding rows, one page twice, one past the pool."""
     b, rows = 5, 7

@@ -129,3 +129,14 @@ def test_sizes_past_63_bits_refused(library, b, L, H, N, P):
     assert library.m3_linattn_fwd(r, at, at, at, at, 1.0, None, None, None, 0, None, at, None, 0, None) == -1
     assert library.m3_linattn_bwd(r, at, at, at, at, 1.0, None, None, at, None, at, at, at, None, None, 0, None) == -1
     assert library.m3_linattn_step(r, at, at, at, at, 1.0, at, 0, None, at, None) == -1
+
+
+@pytest.mark.parametrize("b,L,H,N,P,cut", [
+    (2, 2048, 24, 64, 64, False), (1, 4096, 80, 64, 64, False), (1, 4096, 40, 128, 128, False),
+    (1, 8192, 80, 128, 64, False), (1, 16384, 8, 64, 64, True), (1, 4096, 4, 128, 128, True)])
+def test_sequences_are_cut_where_it_pays(library, b, L, H, N, P, cut):
+    """Sequences that fill a good part of the SMs as they are lose by being cut into segments, up to 4.8 times."""
+    import ctypes
+    d, n = m3.make_dims(b, L, H, P, N, 1, 1, "bf16", chunk=0), ctypes.c_size_t()
+    assert library.m3_linattn_workspace_size(ctypes.byref(d), ctypes.byref(n)) == 0
+    assert (n.value > 0) == cut
