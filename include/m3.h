@@ -369,7 +369,7 @@ m3_status m3_linattn_bwd(const m3_dims* dims, const void* q, const void* k, cons
 typedef struct {
   int32_t npages;                   /* rows of every buffer */
   int32_t nbuf;                     /* buffers, 1 .. M3_PAGES_MAX_BUF */
-  void* base[M3_PAGES_MAX_BUF];     /* device memory, 16-byte aligned, no two overlapping */
+  void* base[M3_PAGES_MAX_BUF];     /* device memory, 16-byte aligned; two that overlap are refused */
   int64_t bytes[M3_PAGES_MAX_BUF];  /* bytes of a row: a positive multiple of 16 */
 } m3_pages;
 

@@ -240,10 +240,18 @@ LaBwd la_backward(const m3_dims* d) {
 m3_status check_pool(const m3_pages* p, int64_t n) {
   if (!p) return M3_ERR_NULL;
   if (p->npages < 0 || p->nbuf < 1 || p->nbuf > M3_PAGES_MAX_BUF || n < 0) return M3_ERR_DIMS;
+  uintptr_t end[M3_PAGES_MAX_BUF];
   for (int j = 0; j < p->nbuf; ++j) {
     if (p->bytes[j] < 16 || p->bytes[j] % 16 != 0) return M3_ERR_DIMS;
     if (p->npages > 0 && !p->base[j]) return M3_ERR_NULL;
     if (!aligned16(p->base[j])) return M3_ERR_ALIGN;
+    uintptr_t bytes;
+    const uintptr_t lo = (uintptr_t)p->base[j];
+    if (__builtin_mul_overflow((uintptr_t)p->bytes[j], (uintptr_t)p->npages, &bytes) ||
+        __builtin_add_overflow(lo, bytes, &end[j]))
+      return M3_ERR_DIMS;
+    for (int i = 0; i < j; ++i)  // no two overlap
+      if (lo < end[i] && (uintptr_t)p->base[i] < end[j]) return M3_ERR_DIMS;
   }
   return M3_OK;
 }

@@ -140,3 +140,29 @@ def test_sequences_are_cut_where_it_pays(library, b, L, H, N, P, cut):
     d, n = m3.make_dims(b, L, H, P, N, 1, 1, "bf16", chunk=0), ctypes.c_size_t()
     assert library.m3_linattn_workspace_size(ctypes.byref(d), ctypes.byref(n)) == 0
     assert (n.value > 0) == cut
+
+
+def _struct(npages, *bufs):
+    p = m3.PagesStruct(npages, len(bufs))
+    for j, (base, nbytes) in enumerate(bufs):
+        p.base[j], p.bytes[j] = base, nbytes
+    return p
+
+
+@pytest.mark.parametrize("bufs", [
+    [(1 << 20, 32), (1 << 20, 32)], [(1 << 20, 32), (2 << 20, 32), ((1 << 20) + 112, 16)],
+    [((1 << 20) + 16, 16), (1 << 20, 32)]], ids=["twice", "tail", "inside"])
+def test_overlapping_buffers_refused(library, bufs):
+    """The threads of two buffers that overlap would race on the same bytes."""
+    import ctypes
+    p, at = ctypes.byref(_struct(4, *bufs)), ctypes.c_void_p(1 << 24)
+    assert library.m3_pages_copy(p, 1, at, at, None) == -1
+    assert library.m3_pages_fork(p, at, 1, at, at, None) == -1
+    assert library.m3_pages_free(p, at, 1, at, None) == -1
+    assert library.m3_pages_compact(p, at, at, at, at, None) == -1
+
+
+def test_adjacent_buffers_taken(library):
+    import ctypes
+    p = ctypes.byref(_struct(4, (1 << 20, 32), ((1 << 20) + 128, 16)))
+    assert library.m3_pages_copy(p, 0, None, None, None) == 0
