@@ -311,13 +311,14 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  * Precision: fp32 throughout for fp32 tensors, for sizes outside the tensor-core tiles, for the
  * shortest sequences and in the step.  With bf16 tensors, N, P in {64, 128} and more than 12 to 48
  * tokens (by the direction, the sizes and the heads) the products run on the tensor cores with fp32
- * accumulation, in chunks of 128 tokens: the weighted scores and the copy of the state that q meets are rounded to bf16; the state
- * itself stays fp32 (its updates enter as three bf16 parts, 24 bits).  An output is off by at most 2^-8
- * of the sum of the absolute values of its terms, beside its own rounding to bf16.  With G < H the heads'
- * shares of dq and dk, which may cancel in their sum, keep two bf16 parts of each operand and are summed
- * in fp32: off by at most 2^-14 of the terms' absolute values, and the final rounding.  An
- * infinity or NaN in a token may also reach the other tokens of its chunk, earlier ones included (a
- * masked score is zero, and zero times infinity is not); tokens past a sequence's length never matter.
+ * accumulation, in chunks of 128 tokens: the weighted scores and the copy of the state that q meets
+ * are rounded to bf16; the state itself stays fp32 (its updates enter as three bf16 parts, 24 bits).
+ * An output is off by at most 2^-8 of the sum of the absolute values of its terms, beside its own
+ * rounding to bf16.  With G < H the heads' shares of dq and dk, which may cancel in their sum, keep two
+ * bf16 parts of each operand and are summed in fp32: off by at most 2^-14 of the terms' absolute
+ * values, and the final rounding.  An infinity or NaN in a token may also reach the other tokens of its
+ * chunk, earlier ones included (a masked score is zero, and zero times infinity is not); tokens past a
+ * sequence's length never matter.
  */
 
 /* Scratch bytes m3_linattn_fwd needs for these dims (0 when it needs none). */
