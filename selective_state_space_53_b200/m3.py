@@ -309,9 +309,14 @@ def _call_stream(index, stream):
     return None
 
 
-def _elsewhere(device, stream):
-    """Context that makes the device current, and `stream` if given (allocations then belong to it too)."""
+def _elsewhere(device, stream, *operands):
+    """Context that makes the device current, and `stream` if given (allocations then belong to it too, and the
+    operands' memory is not handed out again before it has run the call)."""
     import torch
+    if stream is not None:
+        for t in operands:
+            if t is not None:
+                t.record_stream(stream)
     return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
@@ -430,7 +435,7 @@ def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y
         _expect(what, "workspace", workspace, workspace.shape, workspace.dtype, dev)
     raw = _call_stream(dev.index, stream)
     if raw is None:
-        with _elsewhere(dev, stream):
+        with _elsewhere(dev, stream, q, k, v, log_decay, lens, state, pages, y, workspace):
             return linattn(q, k, v, log_decay, scale, lens, state, pages, y, workspace)
     out = state
     if out is None:
@@ -457,7 +462,7 @@ def linattn_step(q, k, v, log_decay, state, scale=None, pages=None, y=None, stre
         _expect(what, "y", y, v.shape, v.dtype, dev)
     raw = _call_stream(dev.index, stream)
     if raw is None:
-        with _elsewhere(dev, stream):
+        with _elsewhere(dev, stream, q, k, v, log_decay, state, pages, y):
             return linattn_step(q, k, v, log_decay, state, scale, pages, y)
     if y is None:
         y = torch.empty_like(v)
@@ -481,7 +486,7 @@ def linattn_backward(q, k, v, log_decay, dy, scale=None, lens=None, state0=None,
             _expect(what, name, t, (dims.b, dims.H, dims.N, dims.P), torch.float32, dev)
     raw = _call_stream(dev.index, stream)
     if raw is None:
-        with _elsewhere(dev, stream):
+        with _elsewhere(dev, stream, q, k, v, log_decay, dy, lens, state0, dstate):
             return linattn_backward(q, k, v, log_decay, dy, scale, lens, state0, dstate)
     out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
            "dstate0": torch.empty((dims.b, dims.H, dims.N, dims.P), dtype=torch.float32, device=dev)}
@@ -535,7 +540,7 @@ class Pages:
             raise M3Error(-1, "Pages.copy: src and dst have different lengths")
         raw = _call_stream(self.device.index, stream)
         if raw is None:
-            with _elsewhere(self.device, stream):
+            with _elsewhere(self.device, stream, src, dst, *self.bufs):
                 return self.copy(src, dst)
         _check(lib().m3_pages_copy(self._ref, n, src.data_ptr(), dst.data_ptr(), raw), "m3_pages_copy")
 
@@ -546,7 +551,7 @@ class Pages:
         n = self._list("Pages.fork", "src", src)
         raw = _call_stream(self.device.index, stream)
         if raw is None:
-            with _elsewhere(self.device, stream):
+            with _elsewhere(self.device, stream, src, self.live, *self.bufs):
                 return self.fork(src)
         dst = torch.empty_like(src)
         _check(lib().m3_pages_fork(self._ref, self.live.data_ptr(), n, src.data_ptr(), dst.data_ptr(), raw),
@@ -558,7 +563,7 @@ class Pages:
         n = self._list("Pages.free", "idx", idx)
         raw = _call_stream(self.device.index, stream)
         if raw is None:
-            with _elsewhere(self.device, stream):
+            with _elsewhere(self.device, stream, idx, self.live):
                 return self.free(idx)
         _check(lib().m3_pages_free(self._ref, self.live.data_ptr(), n, idx.data_ptr(), raw), "m3_pages_free")
 
@@ -568,7 +573,7 @@ class Pages:
         import torch
         raw = _call_stream(self.device.index, stream)
         if raw is None:
-            with _elsewhere(self.device, stream):
+            with _elsewhere(self.device, stream, self.live, *self.bufs):
                 return self.compact()
         n = self.npages
         out = torch.empty((2 * n + 2,), dtype=torch.int32, device=self.device)  # map, order, count

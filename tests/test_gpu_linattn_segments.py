@@ -240,3 +240,23 @@ def test_short_sequences_of_many_heads_keep_fp32(b, L, H, G, N, P):
         check(name, g[name], want, m, c, "bf16")
     check("dstate0", g["dstate0"], ref[3], mag[3], c)
     assert m3.m3_check() == 0
+
+
+def test_operands_freed_after_a_call_on_another_stream():
+    """A temporary operand of a call on a given stream that runs late: its memory is not handed out in between."""
+    dev, _ = draw(2, 40, 4, 2, 64, 64, "bf16", seed=27)
+    ops = [dev[n] for n in ("q", "k", "v")]
+    want, _ = m3.linattn(*ops, dev["ld"])
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)  # about ten milliseconds
+    late = [x.clone() for x in ops]
+    stream.wait_stream(torch.cuda.current_stream())
+    y, _ = m3.linattn(*late, dev["ld"], stream=stream)
+    at = {x.data_ptr() for x in late}
+    del late
+    again = [torch.full_like(x, 3.0) for x in ops for _ in range(4)]
+    assert not at & {x.data_ptr() for x in again}
+    stream.synchronize()
+    assert torch.equal(y, want)

@@ -166,3 +166,57 @@ def test_adjacent_buffers_taken(library):
     import ctypes
     p = ctypes.byref(_struct(4, (1 << 20, 32), ((1 << 20) + 128, 16)))
     assert library.m3_pages_copy(p, 0, None, None, None) == 0
+
+
+def test_operands_of_a_given_stream_are_kept_for_it(monkeypatch):
+    """A call on a stream that is given tells the allocator that its operands are in use there: their memory may
+    not be handed out again on their own stream before the call has read it."""
+    kept = []
+
+    class Operand(Fake):
+        def __getitem__(self, i):
+            return Operand(*self.shape[1:], dtype=self.dtype, device=self.device)
+
+        def record_stream(self, stream):
+            kept.append((id(self), stream))
+
+    class Context:
+        def __init__(self, target):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *exc):
+            return False
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: 0
+
+    monkeypatch.setattr(m3, "lib", lambda: Library())
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+    monkeypatch.setattr(torch, "empty_like", lambda t: t)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: Operand(8))
+    st = Stream(0)
+    prompt = dict(q=Operand(B, T, G, N), k=Operand(B, T, G, N), v=Operand(B, T, H, P), log_decay=Operand(H, **F32))
+    states = Operand(B, H, N, P, **F32)
+    rows = Operand(B, **I32)
+    token = dict(q=Operand(B, G, N), k=Operand(B, G, N), v=Operand(B, H, P), log_decay=Operand(H, **F32))
+    pool = m3.Pages([Operand(4, 8, **F32)], Operand(4, **I32))
+    src, dst = Operand(2, **I32), Operand(2, **I32)
+    calls = [
+        (lambda **kw: m3.linattn(**kw, stream=st),
+         prompt | dict(lens=rows, state=states, pages=Operand(B, **I32), y=Operand(B, T, H, P), workspace=Operand(64))),
+        (lambda **kw: m3.linattn_step(**kw, stream=st), token | dict(state=states, pages=rows, y=Operand(B, H, P))),
+        (lambda **kw: m3.linattn_backward(**kw, stream=st),
+         prompt | dict(dy=Operand(B, T, H, P), lens=rows, state0=states, dstate=Operand(B, H, N, P, **F32))),
+        (lambda **kw: pool.copy(**kw, stream=st), dict(src=src, dst=dst)),
+        (lambda **kw: pool.fork(**kw, stream=st), dict(src=src)),
+        (lambda **kw: pool.free(**kw, stream=st), dict(idx=src))]
+    for call, operands in calls:
+        kept.clear()
+        call(**operands)
+        assert {(id(t), st) for t in operands.values()} <= set(kept)
