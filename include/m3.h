@@ -316,7 +316,8 @@ m3_status m3_output_norm(const m3_dims* dims, const void* y, const void* z, cons
  * An output is off by at most 2^-8 of the sum of the absolute values of its terms, beside its own
  * rounding to bf16.  With G < H the heads' shares of dq and dk, which may cancel in their sum, keep two
  * bf16 parts of each operand and are summed in fp32: off by at most 2^-14 of the terms' absolute
- * values, and the final rounding.  An infinity or NaN in a token may also reach the other tokens of its
+ * values, and the final rounding.  A caller that needs more hands fp32 tensors, which keep fp32
+ * arithmetic at every length.  An infinity or NaN in a token may also reach the other tokens of its
  * chunk, earlier ones included (a masked score is zero, and zero times infinity is not); tokens past a
  * sequence's length never matter.
  */
