@@ -415,9 +415,8 @@ def m3_linattn_bwd(dims: Dims, q, k, v, log_decay, scale, lens, state_in, dy, ds
 def linattn(q, k, v, log_decay, scale=None, lens=None, state=None, pages=None, y=None, workspace=None, stream=None):
     """Linear attention with a decay per head over a batch of sequences (m3_linattn_fwd).
 
-    q, k (b, L, G, N), v (b, L, H, P) bf16 or fp32 (bf16 products on the tensor cores, fp32 arithmetic
-    throughout), G dividing H; log_decay (H) fp32; scale: N ** -0.5
-    if not given; lens (b) int32: the lengths of a padded batch.  state (b, H, N, P) fp32, updated in
+    q, k (b, L, G, N), v (b, L, H, P) in bf16 (products on the tensor cores where the sizes allow) or in fp32
+    (fp32 arithmetic throughout), G dividing H; log_decay (H) fp32; scale: N ** -0.5 if not given; lens (b) int32: the lengths of a padded batch.  state (b, H, N, P) fp32, updated in
     place, or with pages (b) int32 the rows of a pool (npages, H, N, P); without it the sequences are
     fresh.  workspace: a contiguous tensor of m3_linattn_workspace_size bytes on the same device, else
     one is allocated.  Returns (y, state)."""
